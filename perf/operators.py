@@ -313,12 +313,12 @@ def plain_verify(s):
     path[:, 0] = 0
     count = torch.ones(B, dtype=torch.int32, device=DEV)
     for j in range(1, n):
-        tried = par[:, j] == cur
+        tried = (par[:, j] == cur) & (z > 0)
         c = tok[:, j]
         rc = r[b, c]
         qc = q[b, c] if case["dense"] else torch.ones_like(z)
         yes = tried & (u[:, j] * qc * z < rc * w)
-        no = tried & ~yes & (z > 0)
+        no = tried & ~yes
         if case["dense"]:
             t = torch.where(w > 0, 1 / w, 0)
             left = (r * (1 / z)[:, None] - q * t[:, None]).clamp_min(0)
