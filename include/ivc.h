@@ -74,8 +74,15 @@ enum ivc_device_bits {
   IVC_DEV_BAD_OFFSETS = 2,    /* image_offsets not 0 = o0 <= o1 <= ... = T */
   IVC_DEV_WAIT_TIMEOUT = 4,   /* a pipeline barrier wait ran out; outputs invalid */
   IVC_DEV_GROUP_TOO_LARGE = 8, /* a quantile group above IVC_MAX_QUANTILE_GROUP */
-  IVC_DEV_BAD_PROMPT = 16      /* sequence assembly: placeholders != 256 T, a token id
+  IVC_DEV_BAD_PROMPT = 16,     /* sequence assembly: placeholders != 256 T, a token id
                                   outside [0, V) or seq_offsets not 0 <= ... = L */
+  IVC_DEV_BAD_CACHE = 32,      /* a sequence, length, page or token outside the cache,
+                                  a sequence named twice, or a shared page written */
+  IVC_DEV_CACHE_FULL = 64,     /* not enough free pages, or a full page table row */
+  IVC_DEV_BAD_TREE = 128,      /* offsets not 0 = o0 <= o1 <= ... <= N, more than
+                                  IVC_MAX_TREE nodes, or a parent not before its node */
+  IVC_DEV_BAD_PROBS = 256      /* verification: a token id outside [0, V), or a row
+                                  without a finite positive sum to draw from */
 };
 
 #define IVC_MAX_QUANTILE_GROUP 8192
@@ -322,6 +329,156 @@ int ivc_assemble_sequence(const int32_t* input_ids, const int32_t* seq_offsets, 
                           int32_t* out_ids, void* out_embeds, int32_t* out_positions,
                           int32_t* out_seq_offsets, void* workspace, size_t ws_bytes,
                           ivc_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Decoding behind the spliced sequence: a paged cache of keys and values, the
+ * per-head norms and rotation that fill it, the attention that reads it, and
+ * the verification of drafted tokens. One step of a batch:
+ *   ivc_cache_reserve      pages for the new tokens
+ *   per layer: ivc_qk_norm_rope, ivc_tree_attention
+ *   ivc_verify_drafts      which drafted tokens stand, and the next token
+ *   ivc_cache_compact      their keys and values moved together, the rest freed
+ *
+ * The cache. Page p of layer l holds page_tokens tokens of every head; the
+ * tokens of sequence s are, in order, those of pages table[s][0 .. n_pages[s]).
+ * length[s] tokens are committed; new (drafted) tokens stand behind them.
+ * A page may belong to several sequences (ref[p] counts them) once a fork
+ * shared it: such pages are full, and no call writes into them.
+ *   page_tokens 16, 32, 64 or 128; head_dim 64 or 128; pages <= 2^20;
+ *   max_seqs <= 65536; one layer's pages * kv_heads * page_tokens < 2^31.
+ * All pointers are caller-owned device memory; k and v 16-byte aligned.
+ * ivc_cache_init makes every sequence empty and every page free; it leaves k
+ * and v as they are (rows that no token was written to are never used). */
+typedef struct ivc_cache {
+  int layers, pages, kv_heads, page_tokens, head_dim;
+  int max_seqs, max_pages;
+  void* k;             /* bf16 [layers, pages, kv_heads, page_tokens, head_dim] */
+  void* v;             /* the same */
+  int32_t* table;      /* [max_seqs, max_pages]; -1 behind a sequence's pages */
+  int32_t* length;     /* [max_seqs] */
+  int32_t* n_pages;    /* [max_seqs] */
+  int32_t* ref;        /* [pages] */
+  int32_t* free_list;  /* [pages]: free_list[free_count - 1] is taken next */
+  int32_t* free_count; /* [1] */
+} ivc_cache;
+
+#define IVC_MAX_TREE 128           /* drafted nodes of one sequence */
+#define IVC_STEP_WORKSPACE_BYTES 256u /* calls that need the status word only */
+
+int ivc_cache_init(const ivc_cache* c, ivc_stream_t stream);
+
+/* Page operations. `seqs` (device int32 [n], NULL: sequences 0 .. n-1) names
+ * sequences of the cache, each at most once. A call either does all of its
+ * work or, when the device data are wrong (IVC_DEV_BAD_CACHE) or the pages do
+ * not suffice (IVC_DEV_CACHE_FULL), none of it. The results do not depend on
+ * the order in which threads run: pages are taken from the top of the free
+ * list in the order of `seqs`, and given back so that the lowest number of
+ * those freed by the call is taken next.
+ *   reserve  pages for tokens[i] (device int32) more tokens behind length.
+ *   fork     sequence dst[i], which must be empty, becomes a copy of src[i] as
+ *            it stood before the call (committed tokens only). share != 0: full
+ *            pages are shared and only a partly filled last one is copied;
+ *            share == 0: every page is copied.
+ *   compact  the tokens start[i] + keep[i][j], j < count[i], become the tokens
+ *            start[i] + j in every layer, length becomes start[i] + count[i],
+ *            and pages behind that are freed. keep (device int32 [n,
+ *            keep_stride]) rises strictly from >= 0 and may name tokens behind
+ *            length, up to the pages held; NULL keeps the first count[i].
+ *            start (device int32 [n], NULL: length) is at most length. Keys keep
+ *            the rotation they were stored with. A token that would move into a
+ *            shared page, or a shared page that would become the partly
+ *            filled last one, is IVC_DEV_BAD_CACHE (fork without sharing first).
+ *   free     the sequences become empty; pages that no other holds are freed.
+ * reserve and free need IVC_STEP_WORKSPACE_BYTES, fork and compact
+ * ivc_cache_workspace_size(c, n, keep_stride) (0: bad arguments). */
+size_t ivc_cache_workspace_size(const ivc_cache* c, int n, int keep_stride);
+int ivc_cache_reserve(const ivc_cache* c, const int32_t* tokens, const int32_t* seqs, int n,
+                      void* workspace, size_t ws_bytes, ivc_stream_t stream);
+int ivc_cache_fork(const ivc_cache* c, const int32_t* src, const int32_t* dst, int n, int share,
+                   void* workspace, size_t ws_bytes, ivc_stream_t stream);
+int ivc_cache_compact(const ivc_cache* c, const int32_t* count, const int32_t* keep,
+                      int keep_stride, const int32_t* start, const int32_t* seqs, int n,
+                      void* workspace, size_t ws_bytes, ivc_stream_t stream);
+int ivc_cache_free(const ivc_cache* c, const int32_t* seqs, int n, void* workspace,
+                   size_t ws_bytes, ivc_stream_t stream);
+
+/* Norms of queries and keys per head, rotation, and storage in the cache, in
+ * one pass over the packed projections of N token rows. Row i of sequence b
+ * (offsets[b] <= i < offsets[b+1]) holds q_heads query heads, kv_heads key
+ * heads and kv_heads value heads of head_dim. For q and k heads x:
+ *   y = x / sqrt(mean(x^2) + eps) * gamma   (one gamma for q, one for k)
+ *   (out_j, out_{j+D/2}) = (y_j, y_{j+D/2}) rotated by positions[i] theta^(-2j/D)
+ * in fp32 (the angle reduced in fp64), rounded once. Queries go to q_out;
+ * keys and values become token length[s] + i - offsets[b] of sequence
+ * s = seqs[b] (NULL: b) in layer `layer`; `length` itself does not move.
+ *   qkv        device bf16, rows ld elements apart (ld % 8 == 0, at least the
+ *              row's width).
+ *   positions  device int32 [N], e.g. ivc_assemble_sequence's out_positions.
+ *   offsets    device int32 [B+1], 0 = o0 <= o1 <= ... <= oB <= N. Rows from
+ *              oB on (a padded batch) are left as they were.
+ *   q_out      device bf16 [N, q_heads, head_dim].
+ * A token behind the pages that the sequence holds is not stored
+ * (IVC_DEV_BAD_CACHE); bad offsets set IVC_DEV_BAD_TREE. q_heads a multiple of
+ * kv_heads. */
+int ivc_qk_norm_rope(const ivc_cache* c, int layer, const void* qkv, long long ld, int N,
+                     int q_heads, const void* q_gamma, const void* k_gamma, float eps, double theta,
+                     const int32_t* positions, const int32_t* offsets, const int32_t* seqs, int B,
+                     void* q_out, void* workspace, size_t ws_bytes, ivc_stream_t stream);
+
+/* Attention of drafted tokens over the cache. Node i of sequence b's tree (row
+ * offsets[b] + i, at most IVC_MAX_TREE nodes) stands in the cache as token
+ * length[s] + i and sees the length[s] committed tokens, its ancestors and
+ * itself: out = softmax(scale q.k) v over those, q head h with kv head
+ * h / (q_heads / kv_heads). parents[row] is the parent's number within the
+ * tree (< i), or -1: none. parents NULL: each node follows the one before it;
+ * one node per sequence is plain decoding. What a node does not see has no
+ * influence, NaN and infinities included.
+ *   q      device bf16 [N, q_heads, head_dim], rows q_ld elements apart
+ *          (q_ld % 8 == 0).
+ *   out    device bf16 [N, q_heads, head_dim]; rows from offsets[B] on are left
+ *          as they were.
+ * Scores, statistics and sums in fp32; the weights are rounded to bf16 for
+ * their product with v. q_heads / kv_heads <= 64; B <= 4096. A tree with bad
+ * offsets is skipped, a bad parent counts as -1 (IVC_DEV_BAD_TREE); a sequence
+ * whose tokens are not all in its pages is skipped (IVC_DEV_BAD_CACHE). */
+size_t ivc_tree_attention_workspace_size(const ivc_cache* c, int N, int q_heads, int B);
+int ivc_tree_attention(const ivc_cache* c, int layer, const void* q, long long q_ld, int N,
+                       int q_heads, float scale, const int32_t* parents, const int32_t* offsets,
+                       const int32_t* seqs, int B, void* out, void* workspace, size_t ws_bytes,
+                       ivc_stream_t stream);
+
+/* Verification of drafted trees against the target's probabilities, from given
+ * random numbers. Row offsets[b] + i is node i of sequence b: node 0 the last
+ * token that stands, the others drafted tokens; p[row] the target's
+ * distribution of the token after the node, q[row] the distribution that the
+ * node's children were drafted from, one after the other without
+ * replacement (q NULL: the drafts were not drawn at random).
+ * From node 0 with r = p, z = w = 1 the children of the current node are tried
+ * in order. Child j with token c stands iff u[j] q(c) z < r(c) w; then it is
+ * the current node. Else r <- max(r / z - q / w, 0), z <- sum(r), w <- w - q(c),
+ * q(c) <- 0 (q NULL: q(c) = w = 1 in the test, then z <- z - r(c), r(c) <- 0).
+ * After the last standing node the next token is drawn from r: the least v with
+ * sum_{t <= v} r(t) > u_next[b] sum(r). Where sum(r) is 0 it is drawn from the
+ * node's p. A later sibling is not tried once z <= 0. All of this in fp64 from
+ * the fp32 inputs; entries of p and q that are not positive (NaN included)
+ * count as 0.
+ *   p, q    device fp32 [N, V], rows p_ld / q_ld elements apart.
+ *   tokens, parents  device int32 [N]; parents as in ivc_tree_attention
+ *           (NULL: chains), but node 0 is the only root: nodes that do not
+ *           descend from it are never tried.
+ *   u       device fp32 [N] in [0, 1); u_next device fp32 [B].
+ *   path    device int32 [B, path_stride]: the nodes that stand, from node 0
+ *           on, then -1: the keep list of ivc_cache_compact; n_path int32 [B].
+ *   next_token device int32 [B]; -1 (IVC_DEV_BAD_PROBS) where nothing can be
+ *           drawn.
+ * A sequence without nodes gets n_path 0 and next_token -1. path_stride must be
+ * at least 1; a longer path is not walked further. At most IVC_MAX_TREE nodes
+ * per sequence (more, or bad offsets: IVC_DEV_BAD_TREE, as without nodes). */
+int ivc_verify_drafts(const float* p, long long p_ld, const float* q, long long q_ld, int N, int V,
+                      const int32_t* tokens, const int32_t* parents, const int32_t* offsets, int B,
+                      const float* u, const float* u_next, int32_t* path, int path_stride,
+                      int32_t* n_path, int32_t* next_token, void* workspace, size_t ws_bytes,
+                      ivc_stream_t stream);
 
 /* Synchronise `stream`, copy the workspace's device status word to *bits and
  * clear it. Returns IVC_OK when no bit was set, IVC_EDEVICE otherwise. */

@@ -4,6 +4,7 @@ Only ``tests/``, ``__graft_entry__.smoke()`` and the CPU-baseline leg of
 ``bench.py`` import this package. The product path never does.
 """
 from . import ivc_oracle
+from . import decode_oracle
 from .ivc_oracle import *  # noqa: F401,F403
 
 

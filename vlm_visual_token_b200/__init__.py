@@ -8,6 +8,8 @@ functions keep the C names without the ``ivc_`` prefix:
     vir_route(x, valid_len, image_offsets, r)    -> gate, mask, offsets
     route(gate, image_offsets)                   -> mask, offsets, total
     flash_compress(x, valid_len, image_offsets, mlp1, mlp2, r) -> dict
+    assemble_sequence(input_ids, seq_offsets, ...) -> dict
+    Cache, cache_*, qk_norm_rope, tree_attention, verify_drafts: decode.py
 
 Importing this module fails loudly when the shared library is missing; there
 is no fallback implementation.
@@ -21,12 +23,19 @@ from typing import Optional, Sequence
 
 import torch
 
+from .decode import (MAX_TREE, STEP_WORKSPACE_BYTES, Cache, _declare, cache_compact, cache_fork,
+                     cache_free, cache_reserve, cache_workspace_size, qk_norm_rope, tree_attention,
+                     tree_attention_workspace_size, verify_drafts)
+
 POOL_FOLDED, POOL_LITERAL = 0, 1
 
 __all__ = ["Mlp", "Router", "POOL_FOLDED", "POOL_LITERAL", "ps_project", "vir_route", "route",
            "flash_compress", "assemble_sequence", "workspace_size",
            "device_status", "IvcError", "lib", "LIB_PATH", "PS_V1", "PS_QUARTER_TWICE",
-           "OP_PS_HALF", "OP_PS_QUARTER", "OP_VIR_ROUTE", "OP_FLASH"]
+           "OP_PS_HALF", "OP_PS_QUARTER", "OP_VIR_ROUTE", "OP_FLASH", "Cache", "cache_reserve",
+           "cache_fork", "cache_compact", "cache_free", "cache_workspace_size", "qk_norm_rope",
+           "tree_attention", "tree_attention_workspace_size", "verify_drafts", "MAX_TREE",
+           "STEP_WORKSPACE_BYTES"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libivc.so")
 
@@ -123,6 +132,7 @@ def lib() -> ctypes.CDLL:
         L.ivc_trace_reset.argtypes = []
         L.ivc_trace_report.restype = ctypes.c_int
         L.ivc_trace_report.argtypes = [ctypes.c_char_p, ctypes.c_size_t]
+        _declare(L)
         _LIB = L
     return _LIB
 

@@ -19,6 +19,10 @@ constexpr int DEV_BAD_OFFSETS = IVC_DEV_BAD_OFFSETS;
 constexpr int DEV_WAIT_TIMEOUT = IVC_DEV_WAIT_TIMEOUT;
 constexpr int DEV_GROUP_TOO_LARGE = IVC_DEV_GROUP_TOO_LARGE;
 constexpr int DEV_BAD_PROMPT = IVC_DEV_BAD_PROMPT;
+constexpr int DEV_BAD_CACHE = IVC_DEV_BAD_CACHE;
+constexpr int DEV_CACHE_FULL = IVC_DEV_CACHE_FULL;
+constexpr int DEV_BAD_TREE = IVC_DEV_BAD_TREE;
+constexpr int DEV_BAD_PROBS = IVC_DEV_BAD_PROBS;
 
 struct Launch {
   cudaStream_t stream;
@@ -283,6 +287,12 @@ int launch_route(const float* gate, int T, const int32_t* image_offsets, int I, 
 // out[offsets[t] + j] = mask[t] ? Y64[t*64 + j] : Y256[t*256 + j].
 int launch_compact(const bf16* Y256, const bf16* Y64, const uint8_t* mask,
                    const int32_t* offsets, int T, int H, bf16* out, const Launch& L);
+
+// -------------------------------------------------------------- decoding
+// IVC_OK, or why the cache's descriptor is not one (ivc_cache.cu).
+int cache_ok(const ivc_cache* c);
+// The workspace of a call: present, 256-byte aligned, large enough.
+int step_ws_ok(const void* ws, size_t have, size_t need);
 
 // SMs of the current device (queried once per device).
 int num_sms();

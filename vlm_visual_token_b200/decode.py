@@ -1,0 +1,379 @@
+"""Decoding behind the spliced sequence: the paged cache and the calls of one
+decode step (include/ivc.h, "Decoding behind the spliced sequence").
+
+    cache = Cache.empty(layers, pages, kv_heads, page_tokens, head_dim, max_seqs, max_pages)
+    cache_reserve(cache, tokens)                  # pages for the new tokens
+    q = qk_norm_rope(cache, layer, qkv, q_gamma, k_gamma, positions, offsets)
+    out = tree_attention(cache, layer, q, parents, offsets)
+    path, n_path, token = verify_drafts(p, draft_p, tokens, parents, offsets, u, u_next)
+    cache_compact(cache, n_path, path)            # the accepted tokens stay, the rest is freed
+
+Argument marshalling only, as in the rest of the package. A call runs on
+`stream` (default: the current stream of the cache's device), its outputs and
+an omitted workspace are made on that stream. A wrong argument raises IvcError
+before anything is enqueued; wrong device data set bits of the workspace's
+status word (device_status).
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+
+_vp, _i, _ll, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t
+STEP_WORKSPACE_BYTES = 256
+MAX_TREE = 128
+
+
+class _CCache(ctypes.Structure):
+    _fields_ = [(n, _i) for n in ("layers", "pages", "kv_heads", "page_tokens", "head_dim",
+                                  "max_seqs", "max_pages")] + \
+               [(n, _vp) for n in ("k", "v", "table", "length", "n_pages", "ref", "free_list",
+                                   "free_count")]
+
+
+def _declare(L) -> None:
+    P = ctypes.POINTER(_CCache)
+    for name, res, args in (
+            ("ivc_cache_init", _i, [P, _vp]),
+            ("ivc_cache_workspace_size", _sz, [P, _i, _i]),
+            ("ivc_cache_reserve", _i, [P, _vp, _vp, _i, _vp, _sz, _vp]),
+            ("ivc_cache_fork", _i, [P, _vp, _vp, _i, _i, _vp, _sz, _vp]),
+            ("ivc_cache_compact", _i, [P, _vp, _vp, _i, _vp, _vp, _i, _vp, _sz, _vp]),
+            ("ivc_cache_free", _i, [P, _vp, _i, _vp, _sz, _vp]),
+            ("ivc_qk_norm_rope", _i, [P, _i, _vp, _ll, _i, _i, _vp, _vp, ctypes.c_float,
+                                      ctypes.c_double, _vp, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
+            ("ivc_tree_attention_workspace_size", _sz, [P, _i, _i, _i]),
+            ("ivc_tree_attention", _i, [P, _i, _vp, _ll, _i, _i, ctypes.c_float, _vp, _vp, _vp, _i,
+                                        _vp, _vp, _sz, _vp]),
+            ("ivc_verify_drafts", _i, [_vp, _ll, _vp, _ll, _i, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp,
+                                       _i, _vp, _vp, _vp, _sz, _vp])):
+        f = getattr(L, name)
+        f.restype, f.argtypes = res, args
+
+
+def _pkg():
+    import vlm_visual_token_b200 as ivc
+    return ivc
+
+
+def _refuse(what: str, code: int = -1):
+    raise _pkg().IvcError(code, what)
+
+
+def _need(t, what: str, dtype, dims: int, device) -> None:
+    """t is a tensor of this type, rank and device, dense in its last dimension."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != dims or t.device != device:
+        _refuse(f"{what}: a {dims}-dimensional {dtype} tensor on {device} is needed")
+    if t.numel() and not t.is_contiguous():
+        _refuse(f"{what}: not contiguous")
+
+
+def _rows(t, what: str, dtype, device) -> int:
+    """t is a matrix whose rows are dense; the elements between them."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != 2 or t.device != device:
+        _refuse(f"{what}: a 2-dimensional {dtype} tensor on {device} is needed")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        _refuse(f"{what}: rows are not dense")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _at(t) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+@contextlib.contextmanager
+def _other(device, stream):
+    with torch.cuda.device(device):
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
+            yield
+
+
+def _on(device, stream):
+    """Makes `device` and `stream` current for a call, where they are not."""
+    if device.type != "cuda":
+        _refuse("the cache is not on a GPU")
+    if stream is None and device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return _other(device, stream)
+
+
+def _call(name: str, device, *args) -> None:
+    ivc = _pkg()
+    rc = getattr(ivc.lib(), name)(*args, torch.cuda.current_stream(device).cuda_stream)
+    if rc != 0:
+        raise ivc.IvcError(rc, name)
+
+
+def _workspace(ws, need: int, device):
+    if ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        ws[:STEP_WORKSPACE_BYTES].zero_()
+    else:
+        _need(ws, "workspace", torch.uint8, 1, device)
+    return ws
+
+
+class Cache:
+    """Keys and values of many sequences in pages, and the C descriptor.
+
+    k, v: bf16 [layers, pages, kv_heads, page_tokens, head_dim]; the int32 tensors
+    as in include/ivc.h (ivc_cache). Cache.empty() allocates all of them. The
+    tensors are the caller's: the calls below change them in place."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, length: torch.Tensor,
+                 n_pages: torch.Tensor, ref: torch.Tensor, free_list: torch.Tensor,
+                 free_count: torch.Tensor):
+        dev = k.device
+        for name, t in (("k", k), ("v", v)):
+            _need(t, name, torch.bfloat16, 5, dev)
+        if k.shape != v.shape:
+            _refuse("k and v differ in shape")
+        _need(table, "table", torch.int32, 2, dev)
+        seqs = table.shape[0]
+        for name, t, n in (("length", length, seqs), ("n_pages", n_pages, seqs),
+                           ("ref", ref, k.shape[1]), ("free_list", free_list, k.shape[1]),
+                           ("free_count", free_count, 1)):
+            _need(t, name, torch.int32, 1, dev)
+            if t.numel() != n:
+                _refuse(f"{name}: {n} values are needed")
+        self.k, self.v, self.table, self.length, self.n_pages = k, v, table, length, n_pages
+        self.ref, self.free_list, self.free_count = ref, free_list, free_count
+        self.device = dev
+        self.layers, self.pages, self.kv_heads, self.page_tokens, self.head_dim = k.shape
+        self.max_seqs, self.max_pages = table.shape
+        self.c = _CCache(*k.shape, *table.shape, *(t.data_ptr() for t in (
+            k, v, table, length, n_pages, ref, free_list, free_count)))
+        self._p = ctypes.byref(self.c)
+
+    @classmethod
+    def empty(cls, layers: int, pages: int, kv_heads: int, page_tokens: int, head_dim: int,
+              max_seqs: int, max_pages: int, device="cuda", stream=None) -> "Cache":
+        """A cache whose sequences are all empty (ivc_cache_init)."""
+        dev = torch.device(device)
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        with _on(dev, stream):
+            shape = (layers, pages, kv_heads, page_tokens, head_dim)
+            k, v = (torch.empty(shape, dtype=torch.bfloat16, device=dev) for _ in range(2))
+            ints = [torch.empty(s, dtype=torch.int32, device=dev)
+                    for s in ((max_seqs, max_pages), max_seqs, max_seqs, pages, pages, 1)]
+            cache = cls(k, v, *ints)
+            _call("ivc_cache_init", dev, cache._p)
+        return cache
+
+
+def _seqs(cache: Cache, seqs, n: int) -> None:
+    if seqs is not None:
+        _need(seqs, "seqs", torch.int32, 1, cache.device)
+        if seqs.numel() != n:
+            _refuse("seqs: one sequence for each entry is needed")
+
+
+def cache_workspace_size(cache: Cache, n: int, keep_width: int = 0) -> int:
+    """Bytes that cache_fork and cache_compact of n sequences need."""
+    ivc = _pkg()
+    size = ivc.lib().ivc_cache_workspace_size(cache._p, n, keep_width)
+    if size == 0:
+        raise ivc.IvcError(-2, "ivc_cache_workspace_size")
+    return size
+
+
+def cache_reserve(cache: Cache, tokens: torch.Tensor, seqs: Optional[torch.Tensor] = None,
+                  workspace=None, stream=None) -> None:
+    """Pages for tokens[i] more tokens of sequence seqs[i] (default: i)."""
+    _need(tokens, "tokens", torch.int32, 1, cache.device)
+    n = tokens.numel()
+    _seqs(cache, seqs, n)
+    with _on(cache.device, stream):
+        ws = _workspace(workspace, STEP_WORKSPACE_BYTES, cache.device)
+        _call("ivc_cache_reserve", cache.device, cache._p, tokens.data_ptr(), _at(seqs), n,
+              ws.data_ptr(), ws.numel())
+
+
+def cache_fork(cache: Cache, src: torch.Tensor, dst: torch.Tensor, share: bool = True,
+               workspace=None, stream=None) -> None:
+    """Empty sequence dst[i] becomes a copy of src[i]: its full pages shared, or
+    (share=False) every page copied."""
+    for name, t in (("src", src), ("dst", dst)):
+        _need(t, name, torch.int32, 1, cache.device)
+    n = src.numel()
+    if dst.numel() != n:
+        _refuse("src and dst differ in length")
+    with _on(cache.device, stream):
+        ws = _workspace(workspace, cache_workspace_size(cache, n) if workspace is None else 0,
+                        cache.device)
+        _call("ivc_cache_fork", cache.device, cache._p, src.data_ptr(), dst.data_ptr(), n,
+              1 if share else 0, ws.data_ptr(), ws.numel())
+
+
+def cache_compact(cache: Cache, count: torch.Tensor, keep: Optional[torch.Tensor] = None,
+                  start: Optional[torch.Tensor] = None, seqs: Optional[torch.Tensor] = None,
+                  workspace=None, stream=None) -> None:
+    """Tokens start[i] + keep[i, j], j < count[i], become tokens start[i] + j, and
+    the last of them the sequence's last (keep None: the first count[i]; start
+    None: the committed length). Pages behind that are freed."""
+    _need(count, "count", torch.int32, 1, cache.device)
+    n = count.numel()
+    width = 0
+    if keep is not None:
+        _need(keep, "keep", torch.int32, 2, cache.device)
+        if keep.shape[0] != n:
+            _refuse("keep: one row for each count is needed")
+        width = keep.shape[1]
+    if start is not None:
+        _need(start, "start", torch.int32, 1, cache.device)
+        if start.numel() != n:
+            _refuse("start: one value for each count is needed")
+    _seqs(cache, seqs, n)
+    with _on(cache.device, stream):
+        ws = _workspace(workspace, cache_workspace_size(cache, n, width) if workspace is None else 0,
+                        cache.device)
+        # an empty keep has no address: no token can be kept, which count 0 says too
+        _call("ivc_cache_compact", cache.device, cache._p, count.data_ptr(),
+              (_at(keep) or count.data_ptr()) if keep is not None else None, width, _at(start),
+              _at(seqs), n, ws.data_ptr(), ws.numel())
+
+
+def cache_free(cache: Cache, seqs: torch.Tensor, workspace=None, stream=None) -> None:
+    """The sequences become empty; pages that no other sequence holds are freed."""
+    _need(seqs, "seqs", torch.int32, 1, cache.device)
+    with _on(cache.device, stream):
+        ws = _workspace(workspace, STEP_WORKSPACE_BYTES, cache.device)
+        _call("ivc_cache_free", cache.device, cache._p, seqs.data_ptr(), seqs.numel(),
+              ws.data_ptr(), ws.numel())
+
+
+def _batch(offsets, seqs, cache: Cache) -> int:
+    _need(offsets, "offsets", torch.int32, 1, cache.device)
+    B = offsets.numel() - 1
+    if B < 0:
+        _refuse("offsets: at least one value is needed")
+    _seqs(cache, seqs, B)
+    return B
+
+
+def qk_norm_rope(cache: Cache, layer: int, qkv: torch.Tensor, q_gamma: torch.Tensor,
+                 k_gamma: torch.Tensor, positions: torch.Tensor, offsets: torch.Tensor,
+                 theta: float = 1e6, eps: float = 1e-6, seqs: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None, workspace=None, stream=None) -> torch.Tensor:
+    """Per-head norms and rotation of the packed projections qkv [N, (q_heads + 2
+    kv_heads) * head_dim] (rows may be strided); keys and values go to the cache
+    behind the committed tokens, the queries [N, q_heads, head_dim] are returned."""
+    dev, D = cache.device, cache.head_dim
+    ld = _rows(qkv, "qkv", torch.bfloat16, dev)
+    N, width = qkv.shape
+    heads, rest = divmod(width, D)
+    q_heads = heads - 2 * cache.kv_heads
+    if rest or q_heads < 1:
+        _refuse("qkv: q_heads + 2 kv_heads heads of head_dim are needed", -2)
+    for name, t in (("q_gamma", q_gamma), ("k_gamma", k_gamma)):
+        _need(t, name, torch.bfloat16, 1, dev)
+        if t.numel() != D:
+            _refuse(f"{name}: head_dim values are needed")
+    _need(positions, "positions", torch.int32, 1, dev)
+    if positions.numel() != N:
+        _refuse("positions: one for each row is needed")
+    B = _batch(offsets, seqs, cache)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(N, q_heads, D, dtype=torch.bfloat16, device=dev)
+        else:
+            _need(out, "out", torch.bfloat16, 3, dev)
+            if out.shape != (N, q_heads, D):
+                _refuse("out: [N, q_heads, head_dim] is needed")
+        ws = _workspace(workspace, STEP_WORKSPACE_BYTES, dev)
+        _call("ivc_qk_norm_rope", dev, cache._p, layer, qkv.data_ptr(), ld, N, q_heads,
+              q_gamma.data_ptr(), k_gamma.data_ptr(), eps, theta, positions.data_ptr(),
+              offsets.data_ptr(), _at(seqs), B, out.data_ptr(), ws.data_ptr(), ws.numel())
+    return out
+
+
+def tree_attention_workspace_size(cache: Cache, N: int, q_heads: int, B: int) -> int:
+    ivc = _pkg()
+    size = ivc.lib().ivc_tree_attention_workspace_size(cache._p, N, q_heads, B)
+    if size == 0:
+        raise ivc.IvcError(-2, "ivc_tree_attention_workspace_size")
+    return size
+
+
+def tree_attention(cache: Cache, layer: int, q: torch.Tensor, parents: Optional[torch.Tensor],
+                   offsets: torch.Tensor, seqs: Optional[torch.Tensor] = None,
+                   scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                   workspace=None, stream=None) -> torch.Tensor:
+    """Attention of the trees' nodes q [N, q_heads, head_dim] (tokens may be
+    strided) over their committed tokens, ancestors and themselves. parents None:
+    chains. scale: 1 / sqrt(head_dim) by default."""
+    dev, D = cache.device, cache.head_dim
+    if not isinstance(q, torch.Tensor) or q.dtype != torch.bfloat16 or q.dim() != 3 or \
+            q.device != dev or q.shape[2] != D:
+        _refuse(f"q: a bf16 tensor [N, q_heads, {D}] on {dev} is needed")
+    N, q_heads, _ = q.shape
+    if q.numel() and (q.stride(2) != 1 or (q_heads > 1 and q.stride(1) != D)):
+        _refuse("q: a token's heads are not dense")
+    ld = q.stride(0) if N > 1 else q_heads * D
+    if parents is not None:
+        _need(parents, "parents", torch.int32, 1, dev)
+        if parents.numel() != N:
+            _refuse("parents: one for each row is needed")
+    B = _batch(offsets, seqs, cache)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(N, q_heads, D, dtype=torch.bfloat16, device=dev)
+        else:
+            _need(out, "out", torch.bfloat16, 3, dev)
+            if out.shape != (N, q_heads, D):
+                _refuse("out: [N, q_heads, head_dim] is needed")
+        ws = _workspace(workspace, tree_attention_workspace_size(cache, N, q_heads, B)
+                        if workspace is None else 0, dev)
+        _call("ivc_tree_attention", dev, cache._p, layer, q.data_ptr(), ld, N, q_heads,
+              D ** -0.5 if scale is None else scale, _at(parents), offsets.data_ptr(), _at(seqs), B,
+              out.data_ptr(), ws.data_ptr(), ws.numel())
+    return out
+
+
+def verify_drafts(p: torch.Tensor, q: Optional[torch.Tensor], tokens: torch.Tensor,
+                  parents: Optional[torch.Tensor], offsets: torch.Tensor, u: torch.Tensor,
+                  u_next: torch.Tensor, out: Optional[Tuple[torch.Tensor, ...]] = None,
+                  path_width: int = MAX_TREE, workspace=None, stream=None):
+    """Drafted trees against the target's probabilities p [N, V] (rows may be
+    strided), q the probabilities they were drafted from, or None. Returns
+    (path [B, path_width] int32, n_path [B], next_token [B])."""
+    dev = p.device
+    p_ld = _rows(p, "p", torch.float32, dev)
+    N, V = p.shape
+    q_ld = 0
+    if q is not None:
+        q_ld = _rows(q, "q", torch.float32, dev)
+        if q.shape != p.shape:
+            _refuse("p and q differ in shape")
+    for name, t, dtype in (("tokens", tokens, torch.int32), ("parents", parents, torch.int32),
+                           ("u", u, torch.float32)):
+        if t is None and name == "parents":
+            continue
+        _need(t, name, dtype, 1, dev)
+        if t.numel() != N:
+            _refuse(f"{name}: one for each row is needed")
+    _need(offsets, "offsets", torch.int32, 1, dev)
+    _need(u_next, "u_next", torch.float32, 1, dev)
+    B = offsets.numel() - 1
+    if B < 0 or u_next.numel() != B:
+        _refuse("u_next: one for each sequence is needed")
+    with _on(dev, stream):
+        if out is None:
+            out = (torch.empty(B, path_width, dtype=torch.int32, device=dev),
+                   torch.empty(B, dtype=torch.int32, device=dev),
+                   torch.empty(B, dtype=torch.int32, device=dev))
+        path, n_path, token = out
+        _need(path, "path", torch.int32, 2, dev)
+        for name, t in (("n_path", n_path), ("next_token", token)):
+            _need(t, name, torch.int32, 1, dev)
+            if t.numel() != B or path.shape[0] != B:
+                _refuse("out: one entry for each sequence is needed")
+        ws = _workspace(workspace, STEP_WORKSPACE_BYTES, dev)
+        _call("ivc_verify_drafts", dev, p.data_ptr(), p_ld, _at(q), q_ld, N, V, tokens.data_ptr(),
+              _at(parents), offsets.data_ptr(), B, u.data_ptr(), u_next.data_ptr(), path.data_ptr(),
+              path.shape[1], n_path.data_ptr(), token.data_ptr(), ws.data_ptr(), ws.numel())
+    return out
