@@ -1,13 +1,43 @@
-// ivc_tree_attend.cu — attention of drafted trees over the paged cache.
+// ivc_tree_attend.cu — attention of drafted trees over the paged cache, on the
+// 5th-generation tensor cores.
 //
 // out_i = sum_j softmax_j(scale q_i . k_j) v_j over the committed tokens, the
 // node's ancestors and the node itself. One pass with the running maximum m and
-// sum l: per 128 keys m' = max(m, max s), l' = l e^(m - m') + sum e^(s - m'),
-// o' = o e^(m - m') + sum e^(s - m') v; out = o / l.
+// sum l: per tile of 128 keys p = e^(s - m), l = sum p, o = sum p v, all rescaled
+// by e^(m - m') when the maximum rises to m'; out = o / l.
 //
-// A CTA takes one (node, query head): thread t scores key t of a tile, then
-// accumulates value column t. Keys that the node does not see are skipped, not
-// multiplied by zero, so what stands in them has no influence.
+// What bounds it: a (sequence, kv head)'s keys and values are read from HBM once
+// for up to 256 query rows (node x query head of the group), 4 D bytes a key
+// against 4 D operations a row and key, so the read is the bound up to about 250
+// rows, and the shape of the kernel follows the read:
+//   - every CTA (one per SM, persistent) takes the same number of key tiles, a
+//     contiguous piece of the list of all (sequence, row block, kv head, tile):
+//     long and short sequences are cut wherever the pieces end, and the parts of
+//     a cut item are merged by a second kernel in part order;
+//   - keys and values come by TMA, one box per page, into a ring of 160 KB;
+//   - two groups of four softmax warps keep the tensor core and the exponential
+//     unit busy at the same time: with more than 128 query rows each group has
+//     128 rows and every tile; with fewer (plain decoding) both have the same
+//     rows and every other tile, and the groups' results are merged at the end.
+// Per group and tile: S[128 rows x 128 keys] = Q K^T (M 128, N 128), S read from
+// TMEM (thread = row), p written back over S as bf16 and used as the A operand of
+// O[128 x D] += P V (V read MN-major). O stays in TMEM; it is rescaled only when a
+// row's maximum rose by more than 2^8 (p then reaches 2^8 at most, which bf16 and
+// the fp32 sums hold as exactly as values below 1).
+//
+// Rounding: p to bf16 for the product with v (the sum l takes the unrounded p);
+// everything else is fp32 until the output.
+//
+// What a node does not see has no influence: unseen scores become -inf by
+// selection, and in tiles that reach behind the committed tokens one warp first
+// clears value rows behind the sequence and replaces non-finite values of drafted
+// tokens by 0 in shared memory (0 x inf would reach every row); rows that do see
+// such a token get the non-finite value back in the epilogue.
+//
+// Warp 8 loads, warp 9 issues the MMAs from one thread, warp 10 mends value tiles,
+// warps 0-3 and 4-7 are the softmax groups. Every wait is bounded
+// (IVC_DEV_WAIT_TIMEOUT).
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "ivc_internal.h"
@@ -16,112 +46,813 @@
 namespace ivc {
 namespace {
 
-constexpr int TA_KEYS = 128;
+constexpr int TA_THREADS = 352;
+constexpr int TA_KEYS = 128;                 // keys of a tile
+constexpr int TA_ROWS = 128;                 // query rows of a group
+constexpr uint32_t TA_HALF = 128 * 128;      // 128 rows x 64 values
+constexpr int TA_MAX_BATCH = 4096;
+constexpr int TA_MAX_GRID = 256;              // CTAs, one per SM
+constexpr float TA_RISE = 8.f;               // log2 of the rise of m that rescales
 
 struct TreeArgs {
-  const bf16* q;
-  long long q_ld;
-  int N, q_heads, layer, B;
-  float scale;
+  int N, q_heads, group, npt;                // npt: nodes of a 128-row tile
+  int layer, B;
+  float scale_log2;                          // scale * log2(e)
   const int32_t* parents;
   const int32_t* offsets;
   const int32_t* seqs;
   bf16* out;
   int* status;
+  // plan, in the workspace
+  long long* prefix;                         // [B + 1] tiles before sequence b
+  int4* info;                                // [B] {first row, nodes, committed, sequence}
+  int* start;                                // [grid] sequence in which a CTA's piece begins
+  int4* head;                                // [2 grid] an item begun and not ended by a CTA
+  float2* part_ml;                           // [2 grid][256] maximum (log2 units) and sum
+  float* part_o;                             // [2 grid][256][D]
 };
 
-template <int D>
-__global__ void __launch_bounds__(TA_KEYS)
-    tree_attend_kernel(const __grid_constant__ ivc_cache c, const __grid_constant__ TreeArgs a) {
-  __shared__ float s_q[D], s_p[TA_KEYS], s_red[TA_KEYS / 32];
-  __shared__ uint8_t s_sees[IVC_MAX_TREE];
-  __shared__ long long s_row[TA_KEYS];
+__device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
+
+// ------------------------------------------------------------------ plan
+// One CTA: which tiles there are, and the sequence in which each piece begins.
+__global__ void __launch_bounds__(1024)
+    tree_plan_kernel(const __grid_constant__ ivc_cache c, const __grid_constant__ TreeArgs a,
+                     int grid) {
+  __shared__ long long s_prefix[TA_MAX_BATCH + 1];
+  __shared__ long long s_warp[32];
   pdl_wait();
   pdl_trigger();
-  const int row = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
-  if (row == 0 && h == 0)
-    for (int b = tid; b < a.B; b += TA_KEYS)
-      if (a.offsets[b + 1] < a.offsets[b] || a.offsets[b + 1] > a.N) atomicOr(a.status, DEV_BAD_TREE);
-  if (row >= a.offsets[a.B]) return;
-  int lo = 0, hi = a.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.offsets[mid] <= row) lo = mid; else hi = mid;
-  }
-  const int first = a.offsets[lo], n = a.offsets[lo + 1] - first;
-  const int s = a.seqs ? a.seqs[lo] : lo;
-  if (first < 0 || first > row || n > IVC_MAX_TREE || first + n > a.N || row - first >= n) {
-    if (tid == 0) atomicOr(a.status, DEV_BAD_TREE);
-    return;
-  }
-  if (s < 0 || s >= c.max_seqs || c.length[s] < 0 || c.n_pages[s] > c.max_pages ||
-      static_cast<long long>(c.length[s]) + n > static_cast<long long>(c.n_pages[s]) * c.page_tokens) {
-    if (tid == 0) atomicOr(a.status, DEV_BAD_CACHE);
-    return;
-  }
-  const int len = c.length[s], node = row - first;
-  s_sees[tid] = 0;
-  for (int d = tid; d < D; d += TA_KEYS)
-    s_q[d] = __bfloat162float(a.q[static_cast<long long>(row) * a.q_ld + h * D + d]);
-  __syncthreads();
-  if (tid == 0) {
-    for (int i = node; i >= 0;) {
-      s_sees[i] = 1;
-      const int par = a.parents ? a.parents[first + i] : i - 1;
-      if (par < -1 || par >= i) {
-        atomicOr(a.status, DEV_BAD_TREE);
-        break;
-      }
-      i = par;
-    }
-  }
-  __syncthreads();
-  const int kvh = h / (a.q_heads / c.kv_heads);
-  const bf16* kb = static_cast<const bf16*>(c.k);
-  const bf16* vb = static_cast<const bf16*>(c.v);
-  const int32_t* table = c.table + static_cast<size_t>(s) * c.max_pages;
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  for (int t0 = 0; t0 < len + n; t0 += TA_KEYS) {
-    const int t = t0 + tid;
-    float x = -INFINITY;
-    bool sees = t < len || (t < len + n && s_sees[t - len]);
-    long long at = -1;
-    if (sees) {
-      const int page = table[t / c.page_tokens];
-      if (page >= 0 && page < c.pages)
-        at = ((static_cast<long long>(a.layer) * c.pages + page) * c.kv_heads + kvh) *
-                 c.page_tokens * D + static_cast<long long>(t % c.page_tokens) * D;
-      else
-        atomicOr(a.status, DEV_BAD_CACHE);
-      if (at >= 0) {
-        x = 0.f;
-        for (int d = 0; d < D; ++d) x += s_q[d] * __bfloat162float(kb[at + d]);
-        x *= a.scale;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = div_up(a.B, 1024);
+  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+  long long mine = 0;
+  int bad = tid == 0 && a.offsets[0] != 0 ? DEV_BAD_TREE : 0;
+  for (int b = b0; b < b1; ++b) {
+    const int row = a.offsets[b], n = a.offsets[b + 1] - row;
+    int4 info = make_int4(0, 0, 0, 0);
+    long long tiles = 0;
+    if (row < 0 || n < 0 || n > IVC_MAX_TREE || row > a.N - n) {
+      bad |= DEV_BAD_TREE;
+    } else if (n > 0) {
+      const int s = a.seqs ? a.seqs[b] : b;
+      const bool in = s >= 0 && s < c.max_seqs;
+      const int len = in ? c.length[s] : -1, np = in ? c.n_pages[s] : 0;
+      if (len < 0 || np > c.max_pages ||
+          static_cast<long long>(len) + n > static_cast<long long>(np) * c.page_tokens) {
+        bad |= DEV_BAD_CACHE;
+      } else {
+        info = make_int4(row, n, len, s);
+        tiles = static_cast<long long>(div_up(len + n, TA_KEYS)) * c.kv_heads *
+                div_up(n, 2 * a.npt);
       }
     }
-    s_row[tid] = at;
-    float v = x;
+    a.info[b] = info;
+    s_prefix[b] = mine;  // within the thread; completed below
+    mine += tiles;
+  }
+  if (bad) atomicOr(a.status, bad);
+  long long incl = mine;
 #pragma unroll
-    for (int e = 16; e > 0; e >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, e));
-    if ((tid & 31) == 0) s_red[tid >> 5] = v;
-    __syncthreads();
-    const float m2 = fmaxf(m, fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3])));
-    const float base = m2 == -INFINITY ? 0.f : m2;
-    const float f = expf(m - base);
-    s_p[tid] = at >= 0 ? expf(x - base) : 0.f;
-    __syncthreads();
-    l *= f;
-    o *= f;
-    for (int j = 0; j < TA_KEYS; ++j) {
-      if (s_row[j] < 0) continue;
-      l += s_p[j];
-      if (tid < D) o += s_p[j] * __bfloat162float(vb[s_row[j] + tid]);
-    }
-    m = m2;
-    __syncthreads();
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
   }
-  if (tid < D)
-    a.out[(static_cast<long long>(row) * a.q_heads + h) * D + tid] = __float2bfloat16_rn(o / l);
+  if (lane == 31) s_warp[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine;
+  for (int w = 0; w < warp; ++w) before += s_warp[w];
+  for (int b = b0; b < b1; ++b) {
+    s_prefix[b] += before;
+    a.prefix[b] = s_prefix[b];
+  }
+  if (tid == 1023) {
+    s_prefix[a.B] = before + mine;
+    a.prefix[a.B] = before + mine;
+  }
+  __syncthreads();
+  const long long total = s_prefix[a.B];
+  for (int i = tid; i < grid; i += 1024) {
+    const long long pos = total * i / grid;  // the last sequence that begins at or before it
+    int lo = 0, hi = a.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_prefix[mid] <= pos) lo = mid; else hi = mid;
+    }
+    a.start[i] = lo;
+    a.head[2 * i] = make_int4(0, 0, 0, 0);
+  }
+}
+
+// ------------------------------------------------------------------ items
+// A CTA's part of one (sequence, block of up to 2 npt nodes, kv head).
+struct Item {
+  int row, n, len, seq;   // of the sequence: first row, nodes, committed tokens
+  int h;                  // kv head
+  int node0, nodes;       // of the block
+  int t0, t1;             // key tiles of this part
+  bool rows2;             // more than 128 rows: each group has its own
+  bool begins, ends;      // the part holds the item's first / last tile
+  __device__ int units() const { return rows2 ? 2 * (t1 - t0) : t1 - t0; }
+};
+
+// Walks a CTA's piece; every role of the CTA walks it for itself.
+struct Walk {
+  long long pos, end;
+  int b;
+  __device__ Walk(const TreeArgs& a) {
+    const long long total = a.prefix[a.B];
+    pos = total * blockIdx.x / gridDim.x;
+    end = total * (blockIdx.x + 1) / gridDim.x;
+    b = a.start[blockIdx.x];
+  }
+  __device__ bool next(const ivc_cache& c, const TreeArgs& a, Item& it) {
+    if (pos >= end) return false;
+    while (a.prefix[b + 1] <= pos) ++b;
+    const int4 info = a.info[b];
+    it.row = info.x;
+    it.n = info.y;
+    it.len = info.z;
+    it.seq = info.w;
+    const int tiles = div_up(it.len + it.n, TA_KEYS);
+    const long long at = pos - a.prefix[b];
+    const int q = static_cast<int>(at / tiles);
+    it.t0 = static_cast<int>(at % tiles);
+    it.t1 = static_cast<int>(min(static_cast<long long>(tiles), it.t0 + (end - pos)));
+    it.h = q % c.kv_heads;
+    it.node0 = q / c.kv_heads * 2 * a.npt;
+    it.nodes = min(2 * a.npt, it.n - it.node0);
+    it.rows2 = it.nodes > a.npt;
+    it.begins = it.t0 == 0;
+    it.ends = it.t1 == tiles;
+    pos += it.t1 - it.t0;
+    return true;
+  }
+};
+
+// ------------------------------------------------------------------ tcgen05 pieces
+// D[tmem] (+)= A[tmem, bf16 pairs] * B[smem desc].
+__device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+template <int D>
+struct TaSmem {
+  static constexpr int HALVES = D / 64;
+  static constexpr uint32_t SLOT = HALVES * TA_HALF;    // one tile of keys or values
+  static constexpr int SLOTS = 163840 / SLOT;           // 160 KB
+  static constexpr uint32_t Q = 2 * HALVES * TA_HALF;   // two groups' rows
+  static constexpr uint32_t TOTAL = 1024 + Q + SLOTS * SLOT;
+};
+
+// The keys that row `node` sees in tile t0 as bits: committed tokens, and the
+// node's ancestors and itself (anc) behind them.
+__device__ __forceinline__ void tile_mask(const uint32_t (&anc)[4], int len, int t0,
+                                          uint32_t (&mask)[4]) {
+  const int shift = len - t0;  // tile position of node 0
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int below = shift - 32 * w;  // committed tokens in this word
+    uint32_t m = below >= 32 ? 0xffffffffu : below <= 0 ? 0u : (1u << below) - 1u;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int s = shift + 32 * x - 32 * w;  // anc word x starts at bit s of this word
+      if (s > -32 && s < 32) m |= s >= 0 ? anc[x] << s : anc[x] >> -s;
+    }
+    mask[w] = m;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(TA_THREADS, 1)
+    tree_attend_kernel(const __grid_constant__ CUtensorMap qmap,
+                       const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap,
+                       const __grid_constant__ ivc_cache c, const __grid_constant__ TreeArgs a) {
+  using S = TaSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sq = sm;
+  uint8_t* ring = sm + S::Q;
+  __shared__ __align__(8) uint64_t full[S::SLOTS], empty[S::SLOTS];
+  __shared__ __align__(8) uint64_t qfull, qempty, sfull[2], pready[2], ofull, ofree, mlready;
+  __shared__ __align__(8) uint64_t mend, mended;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_mend_slot, s_mend_tile, s_odd[2];  // s_odd: a drafted value is not finite
+  __shared__ float2 s_ml[TA_ROWS];                    // group 1's maximum and sum
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::SLOTS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&qfull, 1);
+    mbar_init(&qempty, 1);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&sfull[g], 1);
+      mbar_init(&pready[g], 4);
+    }
+    mbar_init(&ofull, 1);
+    mbar_init(&ofree, 8);
+    mbar_init(&mlready, 4);
+    mbar_init(&mend, 1);
+    mbar_init(&mended, 1);
+    s_odd[0] = s_odd[1] = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&qmap);
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+  }
+  if (warp == 9) {
+    tmem_alloc(&s_tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  bool ok = true;
+  pdl_wait();     // the plan; everything before it in the stream
+  pdl_trigger();  // the merge may launch; it waits for this grid
+
+  if (warp == 8) {
+    // ------------------------------------------------------------- producer
+    const int pt = c.page_tokens, per_tile = TA_KEYS / pt;
+    const long long nowhere = static_cast<long long>(c.pages) * c.kv_heads * pt;  // reads as 0
+    Walk walk(a);
+    Item it = {};
+    int loads = 0, items = 0, queries = 0;
+    // one tile of keys or values: lane i has the i-th page of the tile
+    auto load = [&](const CUtensorMap* map, int tile) {
+      const int s = loads % S::SLOTS;
+      if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ((loads / S::SLOTS) & 1) ^ 1))) return false;
+      if (lane == 0) mbar_arrive_expect_tx(&full[s], S::SLOT);
+      __syncwarp();
+      if (lane < per_tile) {
+        const int at = tile * per_tile + lane;
+        long long row = nowhere;
+        if (at < div_up(it.len + it.n, pt)) {
+          const int page = c.table[static_cast<size_t>(it.seq) * c.max_pages + at];
+          if (page >= 0 && page < c.pages)
+            row = (static_cast<long long>(page) * c.kv_heads + it.h) * pt;
+          else
+            atomicOr(a.status, DEV_BAD_CACHE);
+        }
+        uint8_t* dst = ring + s * S::SLOT + lane * pt * 128;
+#pragma unroll
+        for (int hf = 0; hf < S::HALVES; ++hf)
+          tma_load_2d(dst + hf * TA_HALF, map, &full[s], 64 * hf, static_cast<int>(row));
+      }
+      ++loads;
+      return true;
+    };
+    auto load_q = [&]() {
+      if (!__all_sync(0xffffffffu, mbar_wait(&qempty, (items & 1) ^ 1))) return false;
+      if (lane == 0) {
+        const int tiles = it.rows2 ? 2 : 1;
+        mbar_arrive_expect_tx(&qfull, tiles * S::HALVES * a.npt * a.group * 128);
+        for (int g = 0; g < tiles; ++g)
+          for (int hf = 0; hf < S::HALVES; ++hf)
+            tma_load_3d(sq + (g * S::HALVES + hf) * TA_HALF, &qmap, &qfull, 64 * hf,
+                        it.h * a.group, it.row + it.node0 + g * a.npt);
+      }
+      ++queries;
+      __syncwarp();
+      return true;
+    };
+    while (ok && walk.next(c, a, it)) {
+      // in the order in which the MMAs first use them (see there); the queries,
+      // whose buffer the item before holds longest, after the first keys
+      const int ahead = it.rows2 ? 1 : 2, T = it.t1 - it.t0;
+      for (int t = 0; t < ahead && t < T && ok; ++t) ok = load(&kmap, it.t0 + t);
+      if (ok) ok = load_q();
+      for (int t = 0; t < T && ok; ++t) {
+        ok = load(&vmap, it.t0 + t);
+        if (ok && t + ahead < T) ok = load(&kmap, it.t0 + t + ahead);
+      }
+      ++items;
+    }
+    if (!ok) {  // let the copies in flight land
+      for (int i = max(0, loads - S::SLOTS); i < loads; ++i)
+        mbar_wait(&full[i % S::SLOTS], (i / S::SLOTS) & 1);
+      if (queries > 0) mbar_wait(&qfull, (queries - 1) & 1);
+    }
+  } else if (warp == 9) {
+    if (lane == 0) {
+      // ----------------------------------------------------------- MMA issuer
+      // unit u: group u & 1, tile u / 2 (own rows) or u (own tiles). Scores of
+      // unit u + 2 follow the weighted sum of unit u, whose weights lie in the
+      // same columns.
+      const uint32_t idesc_s = idesc_bf16_f32(128, TA_KEYS);
+      const uint32_t idesc_o = idesc_bf16_f32(128, D) | (1u << 16);  // B MN-major
+      Walk walk(a);
+      Item it = {};
+      int loads = 0, items = 0, mends = 0;
+      int np[2] = {0, 0};                    // weights consumed per group
+      while (ok && walk.next(c, a, it)) {
+        const int U = it.units();
+        int kslot = 0, vslot = 0;
+        s_odd[items & 1] = 0;
+        auto take = [&](int& slot) {         // the next load in order
+          slot = loads % S::SLOTS;
+          const bool r = mbar_wait(&full[slot], (loads / S::SLOTS) & 1);
+          ++loads;
+          return r;
+        };
+        auto scores = [&](int u) {
+          const int g = u & 1;
+          if (!it.rows2 || g == 0)
+            if (!take(kslot)) return false;
+          if (u == 0 && !mbar_wait(&qfull, items & 1)) return false;
+          tc_fence_after();
+          const uint32_t qa = smem_u32(sq + (it.rows2 ? g : 0) * S::HALVES * TA_HALF);
+          const uint32_t ka = smem_u32(ring + kslot * S::SLOT);
+#pragma unroll
+          for (int hf = 0; hf < S::HALVES; ++hf) {
+            const uint64_t ad = sw128_kmajor_desc(qa + hf * TA_HALF);
+            const uint64_t bd = sw128_kmajor_desc(ka + hf * TA_HALF);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_bf16(tmem + 128 * g, ad + 2 * kk, bd + 2 * kk, idesc_s, (hf | kk) != 0);
+          }
+          umma_commit(&sfull[g]);
+          if (!it.rows2 || g == 1) umma_commit(&empty[kslot]);
+          if (u == U - 1) umma_commit(&qempty);
+          return true;
+        };
+        ok = scores(0);
+        if (ok && U > 1) ok = scores(1);
+        for (int u = 0; u < U && ok; ++u) {
+          const int g = u & 1, tile = it.t0 + (it.rows2 ? u >> 1 : u);
+          bool mend_it = false;
+          if (!it.rows2 || g == 0) {
+            if (!take(vslot)) { ok = false; break; }
+            mend_it = (tile + 1) * TA_KEYS > it.len;  // reaches behind the committed tokens
+            if (mend_it) {
+              s_mend_slot = vslot;
+              s_mend_tile = tile;
+              mbar_arrive(&mend);
+            }
+          }
+          if (!mbar_wait(&pready[g], np[g]++ & 1)) { ok = false; break; }
+          if (mend_it && !mbar_wait(&mended, mends++ & 1)) { ok = false; break; }
+          if (u == 0 && !mbar_wait(&ofree, (items & 1) ^ 1)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t bd =
+              sw128_mnmajor_desc(smem_u32(ring + vslot * S::SLOT), TA_HALF);
+#pragma unroll
+          for (int kk = 0; kk < TA_KEYS / 16; ++kk)
+            umma_bf16_ta(tmem + 256 + 128 * g, tmem + 128 * g + 8 * kk,
+                         bd + ((2048 * kk) >> 4), idesc_o, (u >= 2 || kk != 0) ? 1u : 0u);
+          if (!it.rows2 || g == 1) umma_commit(&empty[vslot]);
+          if (u == U - 1) umma_commit(&ofull);
+          if (u + 2 < U) ok = scores(u + 2);
+        }
+        ++items;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ------------------------------------------------- value tiles at the end
+    Walk walk(a);
+    Item it = {};
+    int mends = 0, items = 0;
+    while (ok && walk.next(c, a, it)) {
+      for (int tile = max(it.t0, it.len / TA_KEYS); tile < it.t1 && ok; ++tile) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&mend, mends & 1));
+        if (!ok) break;
+        ++mends;
+        uint8_t* v = ring + s_mend_slot * S::SLOT;
+        const int base = s_mend_tile * TA_KEYS;
+        const int drafted = max(0, it.len - base);                    // first drafted row
+        const int behind = min(TA_KEYS, it.len + it.n - base);       // first row behind them
+        const int pages_end = min(TA_KEYS, div_up(it.len + it.n, c.page_tokens) * c.page_tokens - base);
+        bool odd = false;
+        // 16-byte pieces; the swizzle only permutes pieces within a row
+        for (int i = lane; i < (pages_end - drafted) * 8; i += 32) {
+          const int r = drafted + (i >> 3);
+#pragma unroll
+          for (int hf = 0; hf < S::HALVES; ++hf) {
+            uint4* at = reinterpret_cast<uint4*>(v + hf * TA_HALF + r * 128 + (i & 7) * 16);
+            if (r >= behind) {
+              *at = make_uint4(0u, 0u, 0u, 0u);
+              continue;
+            }
+            uint4 x = *at;
+            uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+            bool here = false;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if ((w[j] & 0x7f80u) == 0x7f80u) { w[j] &= 0xffff0000u; here = true; }
+              if ((w[j] & 0x7f800000u) == 0x7f800000u) { w[j] &= 0x0000ffffu; here = true; }
+            }
+            if (here) {
+              *at = x;
+              odd = true;
+            }
+          }
+        }
+        if (odd) s_odd[items & 1] = 1;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&mended);
+      }
+      ++items;
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------ softmax, epilogue
+    const int g = warp >> 2, quad = warp & 3;
+    const int r = quad * 32 + lane;                   // row of the group = TMEM lane
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t ts = tmem + lanes + 128 * g, to = tmem + lanes + 256 + 128 * g;
+    const int first_lane_row = quad * 32;
+    Walk walk(a);
+    Item it = {};
+    int items = 0, ns = 0, nml = 0;
+    while (ok && walk.next(c, a, it)) {
+      const int U = it.units();
+      const int node0 = it.node0 + (it.rows2 ? g * a.npt : 0);        // of the group
+      const int gnodes = min(a.npt, it.node0 + it.nodes - node0);
+      const int rows = gnodes * a.group;
+      const bool live = first_lane_row < rows;                        // the warp has rows
+      const int node = node0 + r / a.group;
+      uint32_t anc[4] = {0u, 0u, 0u, 0u};
+      if (live && it.t1 * TA_KEYS > it.len) {
+        // parents of nodes 4 lane .. 4 lane + 3 in the bytes of one register
+        uint32_t packed = 0;
+        bool bad = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = 4 * lane + e;
+          int par = i - 1;
+          if (i < it.n && a.parents) {
+            par = a.parents[it.row + i];
+            if (par < -1 || par >= i) { par = -1; bad = true; }
+          }
+          packed |= static_cast<uint32_t>(par & 0xff) << (8 * e);
+        }
+        if (bad) atomicOr(a.status, DEV_BAD_TREE);
+        int i = r < rows ? node : -1;
+        while (__any_sync(0xffffffffu, i >= 0)) {
+          const int at = max(i, 0);
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            if (i >= 0 && (at >> 5) == w) anc[w] |= 1u << (at & 31);
+          const uint32_t four = __shfl_sync(0xffffffffu, packed, at >> 2);
+          const int par = static_cast<int8_t>((four >> (8 * (at & 3))) & 0xff);
+          i = i < 0 ? -1 : par;
+        }
+      }
+      float m = -INFINITY, l = 0.f;   // the maximum that p is taken against, in log2 units
+      for (int u = g; u < U && ok; u += 2) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&sfull[g], ns & 1));
+        if (!ok) break;
+        ++ns;
+        tc_fence_after();
+        if (live) {
+          const int tile = it.t0 + (it.rows2 ? u >> 1 : u);
+          const bool masked = (tile + 1) * TA_KEYS > it.len;
+          uint32_t mask[4] = {~0u, ~0u, ~0u, ~0u};
+          if (masked) tile_mask(anc, it.len, tile * TA_KEYS, mask);
+          uint32_t x0[32], x1[32];
+          float top = -INFINITY;
+          auto biggest = [&](uint32_t (&x)[32], uint32_t keep) {
+            if (masked) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!((keep >> j) & 1)) x[j] = 0xff800000u;  // -inf
+            }
+            float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              t0 = fmaxf(t0, __uint_as_float(x[j]));
+              t1 = fmaxf(t1, __uint_as_float(x[j + 1]));
+            }
+            top = fmaxf(top, fmaxf(t0, t1));
+          };
+          // the second half of the keys first: the weights of the first half
+          // then overwrite scores that are in registers
+          tmem_ld32(ts + 64, x0);
+          tmem_ld32(ts + 96, x1);
+          tmem_ld_wait();
+          biggest(x0, mask[2]);
+          biggest(x1, mask[3]);
+          tmem_ld32(ts, x0);
+          tmem_ld32(ts + 32, x1);
+          tmem_ld_wait();
+          biggest(x0, mask[0]);
+          biggest(x1, mask[1]);
+          const float rise = top * a.scale_log2;
+          if (u < 2) {
+            m = rise;
+          } else if (__any_sync(0xffffffffu, rise - m > TA_RISE)) {
+            // every earlier sum of this group is complete: its scores followed it
+            const float m2 = fmaxf(m, rise);
+            const float f = m2 == -INFINITY ? 1.f : ex2(m - m2);
+            m = m2;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < D; d += 32) {
+              uint32_t o[32];
+              tmem_ld32(to + d, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st32(to + d, o);
+            }
+          }
+          const float base = m == -INFINITY ? 0.f : m;
+          float sum0 = 0.f, sum1 = 0.f;
+          uint32_t p[32];
+          auto weights = [&](const uint32_t (&x)[32], int first) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const float e0 = ex2(fmaf(__uint_as_float(x[j]), a.scale_log2, -base));
+              const float e1 = ex2(fmaf(__uint_as_float(x[j + 1]), a.scale_log2, -base));
+              sum0 += e0;
+              sum1 += e1;
+              p[first + j / 2] = pack_bf16(e0, e1);
+            }
+          };
+          weights(x0, 0);
+          weights(x1, 16);
+          tmem_st32(ts, p);
+          tmem_ld32(ts + 64, x0);
+          tmem_ld32(ts + 96, x1);
+          tmem_ld_wait();
+          if (masked) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              if (!((mask[2] >> j) & 1)) x0[j] = 0xff800000u;
+              if (!((mask[3] >> j) & 1)) x1[j] = 0xff800000u;
+            }
+          }
+          weights(x0, 0);
+          weights(x1, 16);
+          tmem_st32(ts + 32, p);
+          l += sum0 + sum1;
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pready[g]);
+      }
+      // ---------------------------------------------------------- epilogue
+      const bool two = !it.rows2 && U > 1;  // both groups have sums of the same rows
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(&ofull, items & 1));
+      if (!ok) break;
+      if (!it.rows2 && g == 1) {  // group 0 merges and writes
+        if (two) {
+          s_ml[r] = make_float2(m, l);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&mlready);
+        }
+        if (lane == 0) mbar_arrive(&ofree);
+        ++items;
+        continue;
+      }
+      if (two) ok = __all_sync(0xffffffffu, mbar_wait(&mlready, nml++ & 1));
+      if (!ok) break;
+      tc_fence_after();
+      if (live) {
+        float m1 = -INFINITY, l1 = 0.f;
+        if (two) {
+          const float2 ml = s_ml[r];
+          m1 = ml.x;
+          l1 = ml.y;
+        }
+        const float m2 = fmaxf(m, m1);
+        const float f0 = m == -INFINITY ? 0.f : ex2(m - m2);
+        const float f1 = m1 == -INFINITY ? 0.f : ex2(m1 - m2);
+        // (a row whose scores are NaN keeps a NaN sum)
+        const float sum = (m == -INFINITY ? l : l * f0) + (m1 == -INFINITY ? l1 : l1 * f1);
+        const bool whole = it.begins && it.ends;
+        const float inv = whole ? 1.f / sum : 1.f;
+        const bool write = r < rows;
+        const int slot = 2 * blockIdx.x + (it.begins ? 1 : 0);
+        const int prow = (it.rows2 ? g * TA_ROWS : 0) + r;
+        bf16* dst = a.out + (static_cast<long long>(it.row + node) * a.q_heads +
+                             it.h * a.group + r % a.group) * D;
+        float* part = a.part_o + (static_cast<size_t>(slot) * 256 + prow) * D;
+        const bool odd = s_odd[items & 1] != 0;
+#pragma unroll 1
+        for (int d = 0; d < D; d += 32) {
+          __syncwarp();
+          uint32_t o[32];
+          tmem_ld32(to + d, o);
+          tmem_ld_wait();
+          if (two) {
+            uint32_t o1[32];
+            tmem_ld32(to + 128 + d, o1);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              o[j] = __float_as_uint((__uint_as_float(o[j]) * f0 + __uint_as_float(o1[j]) * f1) * inv);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * inv);
+          }
+          if (!write) continue;
+          if (odd) {  // non-finite values of drafted tokens that this row sees
+            for (int i = max(0, it.t0 * TA_KEYS - it.len); i < it.n; ++i) {
+              const int t = it.len + i;
+              if (t >= it.t1 * TA_KEYS) break;
+              const uint32_t word = i < 64 ? (i < 32 ? anc[0] : anc[1]) : (i < 96 ? anc[2] : anc[3]);
+              if (!((word >> (i & 31)) & 1)) continue;
+              const int page = c.table[static_cast<size_t>(it.seq) * c.max_pages + t / c.page_tokens];
+              if (page < 0 || page >= c.pages) continue;
+              const bf16* v = static_cast<const bf16*>(c.v) +
+                              (((static_cast<size_t>(a.layer) * c.pages + page) * c.kv_heads + it.h) *
+                                   c.page_tokens + t % c.page_tokens) * D + d;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const float y = __bfloat162float(v[j]);
+                if (!isfinite(y)) o[j] = __float_as_uint(__uint_as_float(o[j]) + y);
+              }
+            }
+          }
+          if (whole) {
+            uint4* to16 = reinterpret_cast<uint4*>(dst + d);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = pack_bf16(__uint_as_float(o[8 * j + 2 * k]), __uint_as_float(o[8 * j + 2 * k + 1]));
+              to16[j] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+            uint4* to16 = reinterpret_cast<uint4*>(part + d);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              to16[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          }
+        }
+        if (write && !whole)
+          a.part_ml[static_cast<size_t>(slot) * 256 + prow] = make_float2(two ? m2 : m, sum);
+      }
+      if (g == 0 && warp == 0 && lane == 0 && it.begins && !it.ends) {
+        // the merge's work: the parts that follow are those of the next CTAs
+        a.head[2 * blockIdx.x] = make_int4(1, it.row, it.node0, it.nodes);
+        a.head[2 * blockIdx.x + 1] =
+            make_int4(it.h, it.rows2, div_up(it.len + it.n, TA_KEYS) - it.t1, 0);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ofree);
+      ++items;
+    }
+  }
+  if (!ok) atomicOr(a.status, DEV_WAIT_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ merge
+// Block (i, y): rows 32 y .. 32 y + 31 of the item that CTA i began and did not
+// end. Its parts are CTA i's and, in order, the first ones of the CTAs after it.
+template <int D>
+__global__ void __launch_bounds__(256)
+    tree_merge_kernel(const __grid_constant__ ivc_cache c, const __grid_constant__ TreeArgs a,
+                      int grid) {
+  pdl_wait();
+  pdl_trigger();
+  const int i = blockIdx.x;
+  const int4 h0 = a.head[2 * i], h1 = a.head[2 * i + 1];
+  if (h0.x != 1) return;
+  constexpr int LANES = D / 4;  // a row's lanes, 4 values each
+  __shared__ int s_slot[TA_MAX_GRID];
+  __shared__ int s_parts;
+  if (threadIdx.x == 0) {
+    s_slot[0] = 2 * i + 1;
+    s_parts = 1;
+  }
+  __syncthreads();
+  {
+    const long long total = a.prefix[a.B];
+    const long long item_end = total * (i + 1) / grid + h1.z;
+    for (int j = i + 1 + threadIdx.x; j < grid; j += 256) {
+      const long long pos = total * j / grid;
+      if (pos >= item_end) break;
+      s_slot[j - i] = pos < total * (j + 1) / grid ? 2 * j : -1;  // -1: an empty piece
+      atomicMax(&s_parts, j - i + 1);
+    }
+  }
+  __syncthreads();
+  const int parts = s_parts;
+  const int v = (threadIdx.x % LANES) * 4;
+  for (int row = blockIdx.y * 32 + threadIdx.x / LANES; row < blockIdx.y * 32 + 32;
+       row += 256 / LANES) {
+    const int g = row / TA_ROWS, r = row % TA_ROWS;
+    const int node = g * a.npt + r / a.group;
+    if ((g > 0 && !h1.y) || r >= a.npt * a.group || node >= h0.w) continue;
+    auto slot = [&](int k) { return static_cast<size_t>(s_slot[k]) * 256 + row; };
+    float m = -INFINITY;
+    for (int k = 0; k < parts; ++k)
+      if (s_slot[k] >= 0) m = fmaxf(m, a.part_ml[slot(k)].x);
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < parts; ++k) {
+      if (s_slot[k] < 0) continue;
+      const float2 ml = a.part_ml[slot(k)];
+      if (ml.x == -INFINITY && ml.y == 0.f) continue;  // it saw nothing in that part
+      const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
+      const float4 x = *reinterpret_cast<const float4*>(a.part_o + slot(k) * D + v);
+      l += ml.y * f;
+      o.x += x.x * f;
+      o.y += x.y * f;
+      o.z += x.z * f;
+      o.w += x.w * f;
+    }
+    const float inv = 1.f / l;
+    bf16* dst = a.out + (static_cast<long long>(h0.y + h0.z + node) * a.q_heads + h1.x * a.group +
+                         r % a.group) * D + v;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o.x * inv, o.y * inv),
+                                                pack_bf16(o.z * inv, o.w * inv));
+  }
+}
+
+int tree_grid() { return num_sms() < TA_MAX_GRID ? num_sms() : TA_MAX_GRID; }
+
+size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
+
+// Places the plan and the parts behind the status word; the bytes needed.
+size_t carve(TreeArgs* a, char* ws, int B, int grid, int D) {
+  size_t at = 256;
+  auto take = [&](size_t bytes) {
+    char* p = ws ? ws + at : nullptr;
+    at += up256(bytes);
+    return p;
+  };
+  char* prefix = take(static_cast<size_t>(B + 1) * 8);
+  char* info = take(static_cast<size_t>(B) * 16);
+  char* start = take(static_cast<size_t>(grid) * 4);
+  char* head = take(static_cast<size_t>(grid) * 32);
+  char* ml = take(static_cast<size_t>(grid) * 2 * 256 * 8);
+  char* o = take(static_cast<size_t>(grid) * 2 * 256 * D * 4);
+  if (a) {
+    a->prefix = reinterpret_cast<long long*>(prefix);
+    a->info = reinterpret_cast<int4*>(info);
+    a->start = reinterpret_cast<int*>(start);
+    a->head = reinterpret_cast<int4*>(head);
+    a->part_ml = reinterpret_cast<float2*>(ml);
+    a->part_o = reinterpret_cast<float*>(o);
+  }
+  return at;
+}
+
+template <int D>
+int run_tree(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
+             const ivc_cache& c, const TreeArgs& a, int grid, cudaStream_t s) {
+  const void* kern = reinterpret_cast<const void*>(tree_attend_kernel<D>);
+  if (const int rc = smem_optin(kern, TaSmem<D>::TOTAL)) return rc;
+  {
+    TraceScope ts("tree.plan", s);
+    if (const int rc = launch_k(tree_plan_kernel, dim3(1), dim3(1024), 0, s, 1, c, a, grid)) return rc;
+  }
+  {
+    TraceScope ts("tree.attend", s);
+    if (const int rc = launch_k(tree_attend_kernel<D>, dim3(grid), dim3(TA_THREADS),
+                                TaSmem<D>::TOTAL, s, 1, qm, km, vm, c, a))
+      return rc;
+  }
+  TraceScope ts("tree.merge", s);
+  return launch_k(tree_merge_kernel<D>, dim3(grid, 8), dim3(256), 0, s, 1, c, a, grid);
 }
 
 }  // namespace
@@ -132,8 +863,8 @@ using namespace ivc;
 extern "C" {
 
 size_t ivc_tree_attention_workspace_size(const ivc_cache* c, int N, int q_heads, int B) {
-  if (cache_ok(c) != IVC_OK || N < 0 || B < 0 || q_heads < 1) return 0;
-  return IVC_STEP_WORKSPACE_BYTES;
+  if (cache_ok(c) != IVC_OK || N < 0 || B < 0 || B > TA_MAX_BATCH || q_heads < 1) return 0;
+  return carve(nullptr, nullptr, B, tree_grid(), c->head_dim);
 }
 
 int ivc_tree_attention(const ivc_cache* c, int layer, const void* q, long long q_ld, int N,
@@ -142,8 +873,9 @@ int ivc_tree_attention(const ivc_cache* c, int layer, const void* q, long long q
                        ivc_stream_t stream) {
   if (const int rc = cache_ok(c)) return rc;
   if (layer < 0 || layer >= c->layers || N < 0 || B < 0 || q_heads < 1) return IVC_EINVAL;
-  if (!(scale > -INFINITY && scale < INFINITY)) return IVC_EINVAL;
-  if (q_heads % c->kv_heads != 0 || q_heads / c->kv_heads > 64 || B > 4096) return IVC_EUNSUPPORTED;
+  if (!(scale > 0.f && scale < INFINITY)) return IVC_EINVAL;
+  if (q_heads % c->kv_heads != 0 || q_heads / c->kv_heads > 64 || B > TA_MAX_BATCH)
+    return IVC_EUNSUPPORTED;
   if (q_ld % 8 != 0 || q_ld < static_cast<long long>(q_heads) * c->head_dim) return IVC_EUNSUPPORTED;
   if (!offsets || (N > 0 && (!q || !out))) return IVC_EINVAL;
   auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
@@ -152,12 +884,41 @@ int ivc_tree_attention(const ivc_cache* c, int layer, const void* q, long long q
                                 ivc_tree_attention_workspace_size(c, N, q_heads, B)))
     return rc;
   if (N == 0 || B == 0) return IVC_OK;
-  const TreeArgs a{static_cast<const bf16*>(q), q_ld, N, q_heads, layer, B, scale, parents, offsets,
-                   seqs, static_cast<bf16*>(out), static_cast<int*>(workspace)};
+  const int D = c->head_dim, grid = tree_grid();
+  TreeArgs a = {};
+  a.N = N;
+  a.q_heads = q_heads;
+  a.group = q_heads / c->kv_heads;
+  a.npt = TA_ROWS / a.group;
+  a.layer = layer;
+  a.B = B;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.parents = parents;
+  a.offsets = offsets;
+  a.seqs = seqs;
+  a.out = static_cast<bf16*>(out);
+  a.status = static_cast<int*>(workspace);
+  carve(&a, static_cast<char*>(workspace), B, grid, D);
+  CUtensorMap qm, km, vm;
+  {
+    const unsigned long long d[3] = {static_cast<unsigned long long>(D),
+                                     static_cast<unsigned long long>(q_heads),
+                                     static_cast<unsigned long long>(N)};
+    const unsigned long long st[2] = {static_cast<unsigned long long>(D) * 2,
+                                      static_cast<unsigned long long>(q_ld) * 2};
+    const unsigned box[3] = {64, static_cast<unsigned>(a.group), static_cast<unsigned>(a.npt)};
+    if (map_bf16(&qm, 3, q, d, st, box) != IVC_OK) return IVC_ECUDA;
+  }
+  const size_t rows = static_cast<size_t>(c->pages) * c->kv_heads * c->page_tokens;
+  for (int kv = 0; kv < 2; ++kv) {
+    const unsigned long long d[2] = {static_cast<unsigned long long>(D), rows};
+    const unsigned long long st[1] = {static_cast<unsigned long long>(D) * 2};
+    const unsigned box[2] = {64, static_cast<unsigned>(c->page_tokens)};
+    const bf16* base = static_cast<const bf16*>(kv ? c->v : c->k) + rows * D * layer;
+    if (map_bf16(kv ? &vm : &km, 2, base, d, st, box) != IVC_OK) return IVC_ECUDA;
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  TraceScope ts("tree_attention", s);
-  return launch_k(c->head_dim == 64 ? tree_attend_kernel<64> : tree_attend_kernel<128>,
-                  dim3(N, q_heads), dim3(TA_KEYS), 0, s, 1, *c, a);
+  return D == 64 ? run_tree<64>(qm, km, vm, *c, a, grid, s) : run_tree<128>(qm, km, vm, *c, a, grid, s);
 }
 
 }  // extern "C"
