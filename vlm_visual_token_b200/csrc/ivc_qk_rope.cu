@@ -12,10 +12,11 @@
 // sincospif in fp32. A token's D/2 rotations are computed once and serve all
 // of its heads.
 //
-// Bound by HBM (each value is read and written once). A CTA takes one token: 8
-// bf16 per lane, D/8 lanes per head, so a head's sum of squares and its other
-// half's values are exchanged by shuffles; all 16-byte loads of a thread are
-// issued before the first is used.
+// Bound by HBM (each value is read and written once). Warps work alone: a warp
+// takes a token's heads, or every SPLIT-th batch of them where there are few
+// tokens; 8 bf16 per lane, D/8 lanes per head, so a head's sum of squares and the
+// other half's values come by shuffles. The loads of the first batch are in
+// flight while the warp finds the token's sequence, page and angles.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -27,7 +28,8 @@ namespace ivc {
 namespace {
 
 constexpr int QR_THREADS = 256;
-constexpr int QR_LOADS = 4;  // heads a thread holds at a time
+constexpr int QR_WARPS = QR_THREADS / 32;
+constexpr int QR_LOADS = 4;  // 16-byte loads of a batch, per lane
 
 struct RopeFreq {
   double turn[64];  // f_j / (2 pi)
@@ -36,7 +38,7 @@ struct RopeFreq {
 struct QkArgs {
   const bf16* qkv;
   long long ld;
-  int N, q_heads, layer, B;
+  int N, q_heads, layer, B, split;  // split: warps of a token
   const bf16* gamma_q;
   const bf16* gamma_k;
   float eps;
@@ -65,106 +67,134 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// The sequence that row tok belongs to: the last one that starts at or before it
+// (0 where none does). Each step looks at 32 starts at once.
+__device__ __forceinline__ int seq_of_row(const int32_t* offsets, int B, int tok, int lane) {
+  int lo = 0, n = B;  // the answer is in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int at = lane * step;
+    const bool starts = at < n && offsets[lo + at] <= tok;
+    const unsigned got = __ballot_sync(0xffffffffu, starts);
+    const int last = got ? 31 - __clz(got) : 0;
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  return lo;
+}
+
 template <int D>
-__global__ void __launch_bounds__(QR_THREADS)
+__global__ void __launch_bounds__(QR_THREADS, 4)
     qk_norm_rope_kernel(const __grid_constant__ ivc_cache c, const __grid_constant__ QkArgs a,
                         const __grid_constant__ RopeFreq freq) {
-  constexpr int LANES = D / 8;                      // lanes per head
-  constexpr int AT_ONCE = QR_THREADS / LANES;       // heads per pass of the CTA
-  __shared__ float s_cos[D / 2], s_sin[D / 2];
-  __shared__ long long s_row;                       // first value of the token in its page, or -1
+  constexpr int LANES = D / 8;               // lanes per head
+  constexpr int HEADS = 32 / LANES;          // heads of one load of the warp
+  constexpr int BATCH = HEADS * QR_LOADS;
   pdl_wait();
   pdl_trigger();
-  const int tok = blockIdx.x;
-  if (tok == 0) {
+  const int lane = threadIdx.x & 31;
+  const int unit = blockIdx.x * QR_WARPS + (threadIdx.x >> 5);
+  const int tok = unit / a.split, part = unit % a.split;
+  if (blockIdx.x == 0) {
     for (int b = threadIdx.x; b < a.B; b += QR_THREADS)
       if (a.offsets[b + 1] < a.offsets[b] || a.offsets[b + 1] > a.N) atomicOr(a.status, DEV_BAD_TREE);
     if (threadIdx.x == 0 && a.offsets[0] != 0) atomicOr(a.status, DEV_BAD_TREE);
   }
-  if (tok >= a.offsets[a.B]) return;  // behind the last sequence
-  if (threadIdx.x < D / 2) {
-    double t = a.positions[tok] * freq.turn[threadIdx.x];
-    t -= rint(t);
-    float sn, cs;
-    sincospif(static_cast<float>(2.0 * t), &sn, &cs);
-    s_cos[threadIdx.x] = cs;
-    s_sin[threadIdx.x] = sn;
-  } else if (threadIdx.x == QR_THREADS - 1) {
-    // the sequence that row tok belongs to: the last one that starts at or before it
-    int lo = 0, hi = a.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.offsets[mid] <= tok) lo = mid; else hi = mid;
-    }
-    const int s = a.seqs ? a.seqs[lo] : lo;
-    long long row = -1;
-    if (s >= 0 && s < c.max_seqs && a.offsets[lo] <= tok) {
-      const long long pos = static_cast<long long>(c.length[s]) + tok - a.offsets[lo];
+  if (tok >= a.N) return;
+  const int heads = a.q_heads + 2 * c.kv_heads;
+  const int in_head = lane % LANES;          // 8 values of the head
+  const bf16* src = a.qkv + static_cast<long long>(tok) * a.ld + in_head * 8;
+  const int step = a.split * BATCH;
+  int h0 = part * BATCH + lane / LANES;      // this lane's head of the batch's first load
+  uint4 u[QR_LOADS];
+  auto fetch = [&](int h) {
+#pragma unroll
+    for (int k = 0; k < QR_LOADS; ++k)
+      if (h + k * HEADS < heads)
+        u[k] = *reinterpret_cast<const uint4*>(src + static_cast<long long>(h + k * HEADS) * D);
+      else
+        u[k] = make_uint4(0u, 0u, 0u, 0u);
+  };
+  fetch(h0);
+  const int end = a.offsets[a.B];
+  const int pos = a.positions[tok];
+  const uint4 gq = *reinterpret_cast<const uint4*>(a.gamma_q + in_head * 8);
+  const uint4 gk = *reinterpret_cast<const uint4*>(a.gamma_k + in_head * 8);
+  if (tok >= end) return;                    // behind the last sequence
+  // where the token's key and value go: the first value in its page, or -1
+  long long row = -1;
+  {
+    const int b = seq_of_row(a.offsets, a.B, tok, lane);
+    const int first = a.offsets[b], s = a.seqs ? a.seqs[b] : b;
+    if (s >= 0 && s < c.max_seqs && first <= tok) {
+      const long long at = static_cast<long long>(c.length[s]) + tok - first;
       const int np = min(c.n_pages[s], c.max_pages);
-      if (pos >= 0 && pos < static_cast<long long>(np) * c.page_tokens) {
-        const int page = c.table[static_cast<size_t>(s) * c.max_pages + pos / c.page_tokens];
+      if (at >= 0 && at < static_cast<long long>(np) * c.page_tokens) {
+        const int page = c.table[static_cast<size_t>(s) * c.max_pages + at / c.page_tokens];
         if (page >= 0 && page < c.pages)
-          row = ((static_cast<long long>(a.layer) * c.pages + page) * c.kv_heads *
-                     c.page_tokens + pos % c.page_tokens) * D;
+          row = ((static_cast<long long>(a.layer) * c.pages + page) * c.kv_heads * c.page_tokens +
+                 at % c.page_tokens) * D;
       }
     }
-    if (row < 0) atomicOr(a.status, DEV_BAD_CACHE);
-    s_row = row;
+    if (row < 0 && lane == 0) atomicOr(a.status, DEV_BAD_CACHE);
   }
-  __syncthreads();
-  const int lane = threadIdx.x % LANES;
-  const bool upper = lane >= LANES / 2;             // the second half of the head
-  const int j0 = (lane % (LANES / 2)) * 8;          // its rotations
-  const int heads = a.q_heads + 2 * c.kv_heads;
-  const bf16* src = a.qkv + static_cast<long long>(tok) * a.ld + lane * 8;
-  const long long head_stride = static_cast<long long>(c.page_tokens) * D;
-  for (int h0 = threadIdx.x / LANES; h0 < (heads + AT_ONCE - 1) / AT_ONCE * AT_ONCE;
-       h0 += AT_ONCE * QR_LOADS) {
-    uint4 u[QR_LOADS];
+  // angles: lane l reduces those of D/64 rotations, a lane needs the 8 of its values
+  float cs[8], sn[8];
+  {
+    constexpr int PER = D / 64;
+    float myc[PER], mys[PER];
 #pragma unroll
-    for (int k = 0; k < QR_LOADS; ++k) {
-      const int h = h0 + k * AT_ONCE;
-      u[k] = h < heads ? *reinterpret_cast<const uint4*>(src + static_cast<long long>(h) * D)
-                       : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < PER; ++i) {
+      double t = pos * freq.turn[lane * PER + i];
+      t -= rint(t);
+      sincospif(static_cast<float>(2.0 * t), &mys[i], &myc[i]);
     }
+    const int from = (in_head % (LANES / 2)) * (8 / PER);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      cs[i] = __shfl_sync(0xffffffffu, myc[i % PER], from + i / PER);
+      sn[i] = __shfl_sync(0xffffffffu, mys[i % PER], from + i / PER);
+      if (in_head < LANES / 2) sn[i] = -sn[i];  // first half: y_j cos - y_{j+D/2} sin
+    }
+  }
+  const long long head_stride = static_cast<long long>(c.page_tokens) * D;
+  const int warp_heads = (heads + HEADS - 1) / HEADS * HEADS;  // the same trips for every lane
+  for (; h0 < warp_heads; h0 += step) {
 #pragma unroll
     for (int k = 0; k < QR_LOADS; ++k) {
-      const int h = h0 + k * AT_ONCE;
-      float x[8], other[8];
-      unpack8(u[k], x);
+      const int h = h0 + k * HEADS;
+      const bool is_q = h < a.q_heads;
+      uint4 y = u[k];
+      float x[8];
+      unpack8(y, x);
       float ss = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
 #pragma unroll
       for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const bool is_q = h < a.q_heads;
-      if (h < a.q_heads + c.kv_heads) {
-        float g[8];
-        unpack8(*reinterpret_cast<const uint4*>((is_q ? a.gamma_q : a.gamma_k) + lane * 8), g);
-        const float r = 1.f / sqrtf(ss * (1.f / D) + a.eps);
+      const float r = 1.f / sqrtf(ss * (1.f / D) + a.eps);
+      float g[8];
+      unpack8(is_q ? gq : gk, g);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] * r * g[i];
+      for (int i = 0; i < 8; ++i) x[i] *= r * g[i];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float other = __shfl_xor_sync(0xffffffffu, x[i], LANES / 2);
+        x[i] = x[i] * cs[i] + other * sn[i];
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) other[i] = __shfl_xor_sync(0xffffffffu, x[i], LANES / 2);
       if (h >= heads) continue;
-      if (h < a.q_heads + c.kv_heads) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float cs = s_cos[j0 + i], sn = upper ? s_sin[j0 + i] : -s_sin[j0 + i];
-          x[i] = x[i] * cs + other[i] * sn;
-        }
-        u[k] = pack8(x);
-      }
       if (is_q) {
-        *reinterpret_cast<uint4*>(a.q_out +
-                                  (static_cast<long long>(tok) * a.q_heads + h) * D + lane * 8) = u[k];
-      } else if (s_row >= 0) {
+        *reinterpret_cast<uint4*>(a.q_out + (static_cast<long long>(tok) * a.q_heads + h) * D +
+                                  in_head * 8) = pack8(x);
+      } else if (row >= 0) {
         const int kv = h - a.q_heads;
-        bf16* page = static_cast<bf16*>(kv < c.kv_heads ? c.k : c.v);
-        *reinterpret_cast<uint4*>(page + s_row + (kv % c.kv_heads) * head_stride + lane * 8) = u[k];
+        const bool is_k = kv < c.kv_heads;
+        if (is_k) y = pack8(x);
+        *reinterpret_cast<uint4*>(static_cast<bf16*>(is_k ? c.k : c.v) + row +
+                                  (is_k ? kv : kv - c.kv_heads) * head_stride + in_head * 8) = y;
       }
     }
+    if (h0 + step < warp_heads) fetch(h0 + step);
   }
 }
 
@@ -181,7 +211,7 @@ extern "C" int ivc_qk_norm_rope(const ivc_cache* c, int layer, const void* qkv, 
   if (const int rc = cache_ok(c)) return rc;
   if (layer < 0 || layer >= c->layers || N < 0 || B < 0 || q_heads < 1) return IVC_EINVAL;
   if (!(eps >= 0.f) || !(theta > 0.0) || std::isinf(theta) || std::isinf(eps)) return IVC_EINVAL;
-  if (q_heads % c->kv_heads != 0 || q_heads > 65536) return IVC_EUNSUPPORTED;
+  if (q_heads % c->kv_heads != 0 || q_heads > 65536 || N > (1 << 28)) return IVC_EUNSUPPORTED;
   if (ld % 8 != 0 ||
       ld < (static_cast<long long>(q_heads) + 2 * c->kv_heads) * c->head_dim)
     return IVC_EUNSUPPORTED;
@@ -192,14 +222,24 @@ extern "C" int ivc_qk_norm_rope(const ivc_cache* c, int layer, const void* qkv, 
   if (const int rc = step_ws_ok(workspace, ws_bytes, IVC_STEP_WORKSPACE_BYTES)) return rc;
   if (N == 0 || B == 0) return IVC_OK;
   RopeFreq f = {};
-  for (int j = 0; j < c->head_dim / 2; ++j)
-    f.turn[j] = std::pow(theta, -2.0 * j / c->head_dim) / 6.283185307179586476925;
-  const QkArgs a{static_cast<const bf16*>(qkv), ld, N, q_heads, layer, B,
+  const double ratio = std::pow(theta, -2.0 / c->head_dim);
+  for (int j = 0; j < c->head_dim / 2; ++j)  // at most seven products from a power
+    f.turn[j] = j % 8 ? f.turn[j - 1] * ratio
+                      : std::pow(theta, -2.0 * j / c->head_dim) / 6.283185307179586476925;
+  // a warp per token, or as many as the token has batches while the tokens alone
+  // do not fill the SMs' warps
+  const int batch = 32 / (c->head_dim / 8) * QR_LOADS;
+  const int batches = (q_heads + 2 * c->kv_heads + batch - 1) / batch;
+  int split = 16 * num_sms() / N;
+  split = split < 1 ? 1 : split > batches ? batches : split;
+  const long long blocks = (static_cast<long long>(N) * split + QR_WARPS - 1) / QR_WARPS;
+  const QkArgs a{static_cast<const bf16*>(qkv), ld, N, q_heads, layer, B, split,
                  static_cast<const bf16*>(q_gamma), static_cast<const bf16*>(k_gamma), eps,
                  positions, offsets, seqs, static_cast<bf16*>(q_out),
                  static_cast<int*>(workspace)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   TraceScope ts("qk_norm_rope", s);
-  return launch_k(c->head_dim == 64 ? qk_norm_rope_kernel<64> : qk_norm_rope_kernel<128>, dim3(N),
+  return launch_k(c->head_dim == 64 ? qk_norm_rope_kernel<64> : qk_norm_rope_kernel<128>,
+                  dim3(static_cast<unsigned>(blocks)),
                   dim3(QR_THREADS), 0, s, 1, *c, a, f);
 }
