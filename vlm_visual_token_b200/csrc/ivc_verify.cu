@@ -3,14 +3,20 @@
 // The walk (definition in ivc.h) tries a node's children in ascending order, and
 // parents stand before their children, so the whole walk is one ascending scan:
 // node j is tried iff its parent is the current node when the scan reaches it.
-// A test needs two probabilities, which are gathered up front; only a rejection
-// with draft probabilities needs a pass over the vocabulary, for the sum of
-// max(r / z - q / w, 0), and the final draw one over the row it ends in.
+// Its tests need two probabilities per node, which are gathered up front; only a
+// rejection with draft probabilities needs a pass over the vocabulary, for the sum
+// of max(r / z - q / w, 0), and the final draw one over the row it ends in (none
+// when its last rejection just made that pass).
 //
 // r is a function of the row's fp32 inputs and the scalars z_i, w_i, c_i of the
-// node's rejections so far, so every pass recomputes it in fp64 from the
-// inputs: nothing is stored and nothing rounded in between. Sums are fp64 in a
-// fixed order.
+// node's rejections so far, so every pass recomputes it in fp64 from the inputs:
+// nothing is stored and nothing rounded in between. Sums are fp64 in a fixed order.
+//
+// A sequence is one cluster of 8 CTAs: each walks for itself (the same scalars) and
+// sums a contiguous eighth of the vocabulary, and the eight sums are exchanged
+// through distributed shared memory. Bound by HBM for a batch (the rows of the
+// nodes with rejections are read once from HBM and again from L2), by the chain
+// of dependent loads (offsets, tokens, probabilities, row) for one sequence.
 #include <cuda_runtime.h>
 
 #include "ivc_internal.h"
@@ -19,7 +25,11 @@
 namespace ivc {
 namespace {
 
-constexpr int VF_THREADS = 1024;
+constexpr int VF_THREADS = 512;
+constexpr int VF_WARPS = VF_THREADS / 32;
+constexpr int VF_CLUSTER = 8;
+constexpr int VF_SMALL = 4096;  // a vocabulary up to this size is one CTA's
+constexpr int VF_BATCH = 8;     // values a thread has in flight
 
 struct VerifyArgs {
   const float* p;
@@ -48,177 +58,288 @@ struct Rejected {
   int n;
 };
 
-// r(v) after the node's rejections. DENSE: with draft probabilities.
-__device__ __forceinline__ double left_of(const float* p, const float* q, int v, const Rejected& rj) {
-  double r = positive(p[v]);
-  if (q != nullptr) {
-    if (rj.n == 0) return r;
-    double d = positive(q[v]);
-    for (int i = 0; i < rj.n; ++i) {
-      r = fmax(r * rj.iz[i] - d * rj.iw[i], 0.0);
-      if (v == rj.token[i]) d = 0.0;
-    }
-  } else {
-    for (int i = 0; i < rj.n; ++i)
-      if (v == rj.token[i]) r = 0.0;
-  }
-  return r;
-}
-
-__device__ double block_sum(double x, double* s_warp) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// r of VF_BATCH tokens v0, v0 + step, ... below `end` after the node's rejections;
+// 0 for the others.
+__device__ __forceinline__ void left_of(const float* p, const float* q, int v0, int step, int end,
+                                        const Rejected& rj, double (&r)[VF_BATCH]) {
+  float pf[VF_BATCH], qf[VF_BATCH];
+  const int n = rj.n;
+  const bool with_q = q != nullptr && n > 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  __syncthreads();
-  if (lane == 0) s_warp[warp] = x;
-  __syncthreads();
-  double sum = 0.0;
-  for (int i = 0; i < VF_THREADS / 32; ++i) sum += s_warp[i];
-  return sum;
+  for (int e = 0; e < VF_BATCH; ++e) {
+    const int v = v0 + e * step;
+    pf[e] = v < end ? p[v] : 0.f;
+    qf[e] = with_q && v < end ? q[v] : 0.f;
+  }
+  double d[VF_BATCH];
+#pragma unroll
+  for (int e = 0; e < VF_BATCH; ++e) {
+    r[e] = positive(pf[e]);
+    d[e] = positive(qf[e]);
+  }
+  for (int i = 0; i < n; ++i) {
+    const double iz = rj.iz[i], iw = rj.iw[i];
+    const int tok = rj.token[i];
+#pragma unroll
+    for (int e = 0; e < VF_BATCH; ++e) {
+      if (with_q) {
+        const double x = r[e] * iz - d[e] * iw;
+        r[e] = x > 0.0 ? x : 0.0;
+      }
+      if (v0 + e * step == tok) {
+        if (with_q) d[e] = 0.0;
+        else r[e] = 0.0;
+      }
+    }
+  }
 }
 
-__global__ void __launch_bounds__(VF_THREADS) verify_kernel(const __grid_constant__ VerifyArgs a) {
+// What the CTAs of a cluster tell each other: the sum of their slice, double
+// buffered by pass.
+struct Sums {
+  double slice[2][VF_CLUSTER];
+};
+
+// This CTA's sum into every CTA of the cluster, and all of them back.
+template <int CL>
+__device__ void exchange(Sums& sums, int pass, double mine) {
+  if (CL == 1) {
+    if (threadIdx.x == 0) sums.slice[pass & 1][0] = mine;
+    __syncthreads();
+    return;
+  }
+  if (threadIdx.x < CL) {
+    const uint32_t local = smem_u32(&sums.slice[pass & 1][cluster_ctarank()]);
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(threadIdx.x));
+    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(remote), "d"(mine) : "memory");
+  }
+  cluster_sync();
+}
+
+template <int CL>
+__global__ void __launch_bounds__(VF_THREADS, 2)
+    verify_kernel(const __grid_constant__ VerifyArgs a) {
   __shared__ Rejected rj;
-  __shared__ double s_warp[32];
+  __shared__ Sums sums;
+  __shared__ double s_seg[VF_WARPS];  // sums of the warps' segments of the slice
+  __shared__ double s_scan[VF_WARPS];
   __shared__ int s_tok[IVC_MAX_TREE], s_par[IVC_MAX_TREE];
-  __shared__ float s_u[IVC_MAX_TREE];
+  __shared__ float s_u[IVC_MAX_TREE], s_p[IVC_MAX_TREE], s_q[IVC_MAX_TREE];
+  __shared__ int s_hit, s_last;
+  if (CL > 1) cluster_sync();  // every CTA of the cluster runs: its shared memory may be written
   pdl_wait();
   pdl_trigger();
-  const int b = blockIdx.x, tid = threadIdx.x;
+  const int b = blockIdx.x / CL, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = CL == 1 ? 0 : static_cast<int>(cluster_ctarank());
   int32_t* path = a.path + static_cast<size_t>(b) * a.path_stride;
   const int first = a.offsets[b], n = a.offsets[b + 1] - first;
-  for (int i = tid; i < a.path_stride; i += VF_THREADS) path[i] = -1;
-  if (first < 0 || n < 0 || n > IVC_MAX_TREE || first > a.N - n) {
-    if (tid == 0) atomicOr(a.status, DEV_BAD_TREE);
-  }
-  if (n < 1 || first < 0 || n > IVC_MAX_TREE || first > a.N - n) {
-    if (tid == 0) {
-      a.n_path[b] = 0;
-      a.next_token[b] = -1;
+  const bool bad = first < 0 || n < 0 || n > IVC_MAX_TREE || first > a.N - n;
+  if (bad || n == 0) {  // the same in every CTA of the cluster
+    if (rank == 0) {
+      for (int i = tid; i < a.path_stride; i += VF_THREADS) path[i] = -1;
+      if (tid == 0) {
+        if (bad) atomicOr(a.status, DEV_BAD_TREE);
+        a.n_path[b] = 0;
+        a.next_token[b] = -1;
+      }
     }
     return;
   }
   if (tid < n) {
     int par = a.parents ? a.parents[first + tid] : tid - 1;
+    int tok = a.tokens[first + tid];
+    s_u[tid] = a.u[first + tid];
+    int flags = 0;
     if (par < -1 || par >= tid) {
-      atomicOr(a.status, DEV_BAD_TREE);
+      flags |= DEV_BAD_TREE;
       par = -1;
     }
-    s_par[tid] = par;
-    int tok = a.tokens[first + tid];
     if (tid > 0 && (tok < 0 || tok >= a.V)) {
-      atomicOr(a.status, DEV_BAD_PROBS);
+      flags |= DEV_BAD_PROBS;
       tok = -1;
     }
+    if (flags && rank == 0) atomicOr(a.status, flags);
+    s_par[tid] = par;
     s_tok[tid] = tok;
-    s_u[tid] = a.u[first + tid];
+    if (par >= 0 && tok >= 0) {
+      s_p[tid] = a.p[static_cast<long long>(first + par) * a.p_ld + tok];
+      s_q[tid] = a.q ? a.q[static_cast<long long>(first + par) * a.q_ld + tok] : 1.f;
+    }
   }
   if (tid == 0) rj.n = 0;
   __syncthreads();
 
+  // this CTA's slice of the vocabulary, and the warp's segment of it
+  const int slice = (a.V + CL - 1) / CL;
+  const int lo = min(a.V, rank * slice), hi = min(a.V, lo + slice);
+  const int seg = (slice + VF_WARPS - 1) / VF_WARPS;
+  const int s0 = min(hi, lo + warp * seg), s1 = min(hi, s0 + seg);
+
   const float* p = a.p + static_cast<long long>(first) * a.p_ld;
   const float* q = a.q ? a.q + static_cast<long long>(first) * a.q_ld : nullptr;
+  int passes = 0;
+  bool summed = false;  // s_seg and sums hold the current r
+  // the sum of r: per segment, per slice, in all
+  auto sum_all = [&]() -> double {
+    double acc[2] = {0.0, 0.0};
+    for (int v = s0 + lane; v < s1; v += 32 * VF_BATCH) {
+      double r[VF_BATCH];
+      left_of(p, q, v, 32, s1, rj, r);
+#pragma unroll
+      for (int e = 0; e < VF_BATCH; ++e) acc[e & 1] += r[e];
+    }
+    double x = acc[0] + acc[1];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (lane == 0) s_seg[warp] = x;
+    __syncthreads();
+    double mine = 0.0;
+#pragma unroll
+    for (int w = 0; w < VF_WARPS; ++w) mine += s_seg[w];
+    exchange<CL>(sums, passes, mine);
+    double all = 0.0;
+#pragma unroll
+    for (int k = 0; k < CL; ++k) all += sums.slice[passes & 1][k];
+    ++passes;
+    summed = true;
+    return all;
+  };
+
+  // the walk: the same in every thread
   int cur = 0, count = 1;
   double z = 1.0, w = 1.0;
-  if (tid == 0) path[0] = 0;
+  if (rank == 0 && tid == 0) path[0] = 0;
   for (int j = 1; j < n && count < a.path_stride; ++j) {
-    if (s_par[j] != cur || !(z > 0.0) || s_tok[j] < 0) continue;
     const int tok = s_tok[j];
-    const double r = left_of(p, q, tok, rj);
-    double d = 1.0;
-    if (q != nullptr) {
-      d = positive(q[tok]);
-      for (int i = 0; i < rj.n; ++i)
-        if (rj.token[i] == tok) d = 0.0;
+    if (s_par[j] != cur || !(z > 0.0) || tok < 0) continue;
+    double r = positive(s_p[j]), d = q != nullptr ? positive(s_q[j]) : 1.0;
+    for (int i = 0; i < rj.n; ++i) {
+      if (q != nullptr) {
+        r = r * rj.iz[i] - d * rj.iw[i];
+        r = r > 0.0 ? r : 0.0;
+      }
+      if (rj.token[i] == tok) {
+        if (q != nullptr) d = 0.0;
+        else r = 0.0;
+      }
     }
-    if (static_cast<double>(s_u[j]) * d * z < r * w) {
+    const bool stands = static_cast<double>(s_u[j]) * d * z < r * w;
+    __syncthreads();  // rj is read
+    if (stands) {
       cur = j;
       p = a.p + static_cast<long long>(first + j) * a.p_ld;
       if (q != nullptr) q = a.q + static_cast<long long>(first + j) * a.q_ld;
       z = w = 1.0;
-      if (tid == 0) path[count] = j;
+      summed = false;
+      if (tid == 0) {
+        rj.n = 0;
+        if (rank == 0) path[count] = j;
+      }
       ++count;
       __syncthreads();
-      if (tid == 0) rj.n = 0;
-      __syncthreads();
     } else {
-      __syncthreads();
       if (tid == 0) {
-        rj.iz[rj.n] = 1.0 / z;
-        rj.iw[rj.n] = w > 0.0 ? 1.0 / w : 0.0;
-        rj.token[rj.n] = tok;
-        ++rj.n;
+        const int k = rj.n;
+        rj.iz[k] = 1.0 / z;
+        rj.iw[k] = w > 0.0 ? 1.0 / w : 0.0;
+        rj.token[k] = tok;
+        rj.n = k + 1;
       }
       __syncthreads();
       if (q != nullptr) {
-        double sum = 0.0;
-        for (int v = tid; v < a.V; v += VF_THREADS) sum += left_of(p, q, v, rj);
-        z = block_sum(sum, s_warp);
+        z = sum_all();
         w -= d;
       } else {
         z -= r;
+        summed = false;
       }
     }
   }
 
-  // the draw: contiguous slices of the row per thread
-  const int per = (a.V + VF_THREADS - 1) / VF_THREADS;
-  const int v0 = min(a.V, tid * per), v1 = min(a.V, v0 + per);
-  for (int pass = 0; pass < 2; ++pass) {
-    double mine = 0.0;
-    for (int v = v0; v < v1; ++v) mine += left_of(p, q, v, rj);
-    const double total = block_sum(mine, s_warp);
-    if (!(total > 0.0) && pass == 0 && rj.n > 0) {  // nothing left: the node's own row
-      __syncthreads();
-      if (tid == 0) rj.n = 0;
-      __syncthreads();
-      continue;
-    }
-    int token = -1;
-    if (total > 0.0 && !isinf(total)) {
-      // exclusive sums in thread order
-      __shared__ double s_sum[VF_THREADS];
-      s_sum[tid] = mine;
-
-      __syncthreads();
-      if (tid == 0) {
-        double t = 0.0;
-        for (int i = 0; i < VF_THREADS; ++i) {
-          const double m = s_sum[i];
-          s_sum[i] = t;
-          t += m;
-        }
-        const double goal = static_cast<double>(a.u_next[b]) * t;
-        s_warp[0] = goal;
-      }
-      __syncthreads();
-      const double goal = s_warp[0];
-      double t = s_sum[tid];
-      int last = -1, hit = -1;
-      for (int v = v0; v < v1; ++v) {
-        const double r = left_of(p, q, v, rj);
-        t += r;
-        if (r > 0.0) {
-          last = v;
-          if (hit < 0 && t > goal) hit = v;
-        }
-      }
-      // the least hit, or (a goal that rounding put at the sum) the last value
-      __shared__ int s_hit, s_last;
-      if (tid == 0) { s_hit = a.V; s_last = -1; }
-      __syncthreads();
-      if (hit >= 0) atomicMin(&s_hit, hit);
-      if (last >= 0) atomicMax(&s_last, last);
-      __syncthreads();
-      token = s_hit < a.V ? s_hit : s_last;
-    }
-    if (tid == 0) {
-      if (token < 0) atomicOr(a.status, DEV_BAD_PROBS);
-      a.next_token[b] = token;
-      a.n_path[b] = count;
-    }
-    break;
+  // the draw
+  double total = summed ? z : sum_all();
+  if (!(total > 0.0) && rj.n > 0) {  // nothing left: the node's own row
+    __syncthreads();
+    if (tid == 0) rj.n = 0;
+    __syncthreads();
+    total = sum_all();
   }
+  if (rank == 0) {
+    for (int i = count + tid; i < a.path_stride; i += VF_THREADS) path[i] = -1;
+    if (tid == 0) a.n_path[b] = count;
+  }
+  if (!(total > 0.0) || isinf(total)) {
+    if (rank == 0 && tid == 0) {
+      atomicOr(a.status, DEV_BAD_PROBS);
+      a.next_token[b] = -1;
+    }
+    return;
+  }
+  // the slice, then the segment, in which the running sum passes the goal; where
+  // rounding leaves none, the last one that holds anything
+  const double goal = static_cast<double>(a.u_next[b]) * total;
+  const double* slices = sums.slice[(passes - 1) & 1];
+  double base = 0.0, run = 0.0;
+  int owner = -1, last = 0;
+#pragma unroll
+  for (int k = 0; k < CL; ++k) {
+    const double next = run + slices[k];
+    if (slices[k] > 0.0) {
+      if (owner < 0) { last = k; base = run; }
+      if (owner < 0 && next > goal) owner = k;
+    }
+    run = next;
+  }
+  if (owner < 0) owner = last;
+  if (rank != owner) return;
+  run = base;
+  int part = -1;
+  last = 0;
+  for (int k = 0; k < VF_WARPS; ++k) {
+    const double next = run + s_seg[k];
+    if (s_seg[k] > 0.0) {
+      if (part < 0) { last = k; base = run; }
+      if (part < 0 && next > goal) part = k;
+    }
+    run = next;
+  }
+  if (part < 0) part = last;
+  // that segment once more, in thread order: VF_BATCH neighbouring values each
+  if (tid == 0) { s_hit = a.V; s_last = -1; }
+  const int e0 = lo + part * seg, e1 = min(hi, e0 + seg);
+  run = base;
+  for (int v0 = e0; v0 < e1; v0 += VF_THREADS * VF_BATCH) {
+    const int v = v0 + tid * VF_BATCH;
+    double r[VF_BATCH], mine = 0.0;
+    left_of(p, q, v, 1, e1, rj, r);
+#pragma unroll
+    for (int e = 0; e < VF_BATCH; ++e) mine += r[e];
+    double incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    __syncthreads();
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    double before = run + incl - mine;
+    for (int k = 0; k < VF_WARPS; ++k) {
+      if (k < warp) before += s_scan[k];
+      run += s_scan[k];
+    }
+#pragma unroll
+    for (int e = 0; e < VF_BATCH; ++e) {
+      before += r[e];
+      if (r[e] > 0.0) {
+        atomicMax(&s_last, v + e);
+        if (before > goal) atomicMin(&s_hit, v + e);
+      }
+    }
+  }
+  __syncthreads();
+  if (tid == 0) a.next_token[b] = s_hit < a.V ? s_hit : s_last;
 }
 
 }  // namespace
@@ -234,6 +355,7 @@ extern "C" int ivc_verify_drafts(const float* p, long long p_ld, const float* q,
                                  size_t ws_bytes, ivc_stream_t stream) {
   if (N < 0 || V < 1 || B < 0 || path_stride < 1) return IVC_EINVAL;
   if (p_ld < V || (q && q_ld < V)) return IVC_EINVAL;
+  if (B > (1 << 24) || V > (1 << 28)) return IVC_EUNSUPPORTED;
   if (B > 0 && (!offsets || !u_next || !path || !n_path || !next_token)) return IVC_EINVAL;
   if (N > 0 && (!p || !tokens || !u)) return IVC_EINVAL;
   if (const int rc = step_ws_ok(workspace, ws_bytes, IVC_STEP_WORKSPACE_BYTES)) return rc;
@@ -242,5 +364,7 @@ extern "C" int ivc_verify_drafts(const float* p, long long p_ld, const float* q,
                      path, path_stride, n_path, next_token, static_cast<int*>(workspace)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   TraceScope ts("verify_drafts", s);
-  return launch_k(verify_kernel, dim3(B), dim3(VF_THREADS), 0, s, 1, a);
+  if (V <= VF_SMALL) return launch_k(verify_kernel<1>, dim3(B), dim3(VF_THREADS), 0, s, 1, a);
+  return launch_k(verify_kernel<VF_CLUSTER>, dim3(static_cast<unsigned>(B) * VF_CLUSTER),
+                  dim3(VF_THREADS), 0, s, VF_CLUSTER, a);
 }
