@@ -25,8 +25,6 @@
 namespace ivc {
 namespace {
 
-constexpr int VF_THREADS = 512;
-constexpr int VF_WARPS = VF_THREADS / 32;
 constexpr int VF_CLUSTER = 8;
 constexpr int VF_SMALL = 4096;  // a vocabulary up to this size is one CTA's
 constexpr int VF_BATCH = 8;     // values a thread has in flight
@@ -49,7 +47,7 @@ struct VerifyArgs {
   int* status;
 };
 
-__device__ __forceinline__ double positive(float x) { return x > 0.f ? static_cast<double>(x) : 0.0; }
+__device__ __forceinline__ double positive(float x) { return static_cast<double>(fmaxf(x, 0.f)); }
 
 // The rejections at the current node.
 struct Rejected {
@@ -58,39 +56,53 @@ struct Rejected {
   int n;
 };
 
-// r of VF_BATCH tokens v0, v0 + step, ... below `end` after the node's rejections;
-// 0 for the others.
-__device__ __forceinline__ void left_of(const float* p, const float* q, int v0, int step, int end,
-                                        const Rejected& rj, double (&r)[VF_BATCH]) {
-  float pf[VF_BATCH], qf[VF_BATCH];
-  const int n = rj.n;
-  const bool with_q = q != nullptr && n > 0;
+// max(x, 0) without the fp64 comparison: x is no NaN (or the row has infinities
+// and its sum is refused).
+__device__ __forceinline__ double above_zero(double x) {
+  const int hi = __double2hiint(x), keep = ~(hi >> 31);
+  return __hiloint2double(hi & keep, __double2loint(x) & keep);
+}
+
+// VF_BATCH tokens v0, v0 + step, ... below `end`: their inputs (0 for the others) ...
+struct Batch {
+  float p[VF_BATCH], q[VF_BATCH];
+};
+__device__ __forceinline__ void fetch(const float* p, const float* q, int v0, int step, int end,
+                                      Batch& x) {
 #pragma unroll
   for (int e = 0; e < VF_BATCH; ++e) {
     const int v = v0 + e * step;
-    pf[e] = v < end ? p[v] : 0.f;
-    qf[e] = with_q && v < end ? q[v] : 0.f;
+    x.p[e] = v < end ? p[v] : 0.f;
+    x.q[e] = q != nullptr && v < end ? q[v] : 0.f;
   }
-  double d[VF_BATCH];
-#pragma unroll
-  for (int e = 0; e < VF_BATCH; ++e) {
-    r[e] = positive(pf[e]);
-    d[e] = positive(qf[e]);
-  }
-  for (int i = 0; i < n; ++i) {
-    const double iz = rj.iz[i], iw = rj.iw[i];
-    const int tok = rj.token[i];
+}
+// ... and their r after the node's rejections. With draft probabilities a rejected
+// token needs no exclusion from q here: u q(c) / w >= r(c) / z with u < 1 makes
+// its r 0, and so it stays.
+__device__ __forceinline__ void left_of(const Batch& x, bool dense, int v0, int step,
+                                        const Rejected& rj, double (&r)[VF_BATCH]) {
+  const int n = rj.n;
+  if (dense) {
+    double d[VF_BATCH];
 #pragma unroll
     for (int e = 0; e < VF_BATCH; ++e) {
-      if (with_q) {
-        const double x = r[e] * iz - d[e] * iw;
-        r[e] = x > 0.0 ? x : 0.0;
-      }
-      if (v0 + e * step == tok) {
-        if (with_q) d[e] = 0.0;
-        else r[e] = 0.0;
-      }
+      d[e] = positive(x.q[e]);
+      r[e] = above_zero(positive(x.p[e]) - d[e]);  // the first rejection: z = w = 1
     }
+    for (int i = 1; i < n; ++i) {
+      const double iz = rj.iz[i], iw = rj.iw[i];
+#pragma unroll
+      for (int e = 0; e < VF_BATCH; ++e) r[e] = above_zero(r[e] * iz - d[e] * iw);
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < VF_BATCH; ++e) r[e] = positive(x.p[e]);
+  for (int i = 0; i < n; ++i) {
+    const int tok = rj.token[i];
+#pragma unroll
+    for (int e = 0; e < VF_BATCH; ++e)
+      if (v0 + e * step == tok) r[e] = 0.0;
   }
 }
 
@@ -117,9 +129,10 @@ __device__ void exchange(Sums& sums, int pass, double mine) {
   cluster_sync();
 }
 
-template <int CL>
-__global__ void __launch_bounds__(VF_THREADS, 2)
+template <int CL, int VF_THREADS, int PER_SM>
+__global__ void __launch_bounds__(VF_THREADS, PER_SM)
     verify_kernel(const __grid_constant__ VerifyArgs a) {
+  constexpr int VF_WARPS = VF_THREADS / 32;
   __shared__ Rejected rj;
   __shared__ Sums sums;
   __shared__ double s_seg[VF_WARPS];  // sums of the warps' segments of the slice
@@ -183,9 +196,12 @@ __global__ void __launch_bounds__(VF_THREADS, 2)
   // the sum of r: per segment, per slice, in all
   auto sum_all = [&]() -> double {
     double acc[2] = {0.0, 0.0};
+    const float* qq = rj.n > 0 ? q : nullptr;
     for (int v = s0 + lane; v < s1; v += 32 * VF_BATCH) {
+      Batch x;
+      fetch(p, qq, v, 32, s1, x);
       double r[VF_BATCH];
-      left_of(p, q, v, 32, s1, rj, r);
+      left_of(x, qq != nullptr, v, 32, rj, r);
 #pragma unroll
       for (int e = 0; e < VF_BATCH; ++e) acc[e & 1] += r[e];
     }
@@ -311,8 +327,11 @@ __global__ void __launch_bounds__(VF_THREADS, 2)
   run = base;
   for (int v0 = e0; v0 < e1; v0 += VF_THREADS * VF_BATCH) {
     const int v = v0 + tid * VF_BATCH;
+    const float* qq = rj.n > 0 ? q : nullptr;
+    Batch x;
+    fetch(p, qq, v, 1, e1, x);
     double r[VF_BATCH], mine = 0.0;
-    left_of(p, q, v, 1, e1, rj, r);
+    left_of(x, qq != nullptr, v, 1, rj, r);
 #pragma unroll
     for (int e = 0; e < VF_BATCH; ++e) mine += r[e];
     double incl = mine;
@@ -364,7 +383,12 @@ extern "C" int ivc_verify_drafts(const float* p, long long p_ld, const float* q,
                      path, path_stride, n_path, next_token, static_cast<int*>(workspace)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   TraceScope ts("verify_drafts", s);
-  if (V <= VF_SMALL) return launch_k(verify_kernel<1>, dim3(B), dim3(VF_THREADS), 0, s, 1, a);
-  return launch_k(verify_kernel<VF_CLUSTER>, dim3(static_cast<unsigned>(B) * VF_CLUSTER),
-                  dim3(VF_THREADS), 0, s, VF_CLUSTER, a);
+  // Small vocabularies: one CTA. Otherwise wide CTAs while all clusters are
+  // resident with them (two per SM; one sequence 6.8 against 8.1 us), narrow ones
+  // beyond that (four per SM; 48 sequences without a rejection 12.9 against 16.0).
+  if (V <= VF_SMALL) return launch_k(verify_kernel<1, 384, 2>, dim3(B), dim3(384), 0, s, 1, a);
+  const unsigned ctas = static_cast<unsigned>(B) * VF_CLUSTER;
+  if (ctas <= 2u * num_sms())
+    return launch_k(verify_kernel<VF_CLUSTER, 384, 2>, dim3(ctas), dim3(384), 0, s, VF_CLUSTER, a);
+  return launch_k(verify_kernel<VF_CLUSTER, 256, 4>, dim3(ctas), dim3(256), 0, s, VF_CLUSTER, a);
 }
