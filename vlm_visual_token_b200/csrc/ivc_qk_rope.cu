@@ -13,10 +13,13 @@
 // of its heads.
 //
 // Bound by HBM (each value is read and written once). Warps work alone: a warp
-// takes a token's heads, or every SPLIT-th batch of them where there are few
-// tokens; 8 bf16 per lane, D/8 lanes per head, so a head's sum of squares and the
-// other half's values come by shuffles. The loads of the first batch are in
-// flight while the warp finds the token's sequence, page and angles.
+// takes a token's heads, or every split-th batch of them where there are few
+// tokens. D/8 lanes per head; a lane holds 4 values of the head's first half and
+// the 4 of the second half that they are rotated with, so only the sum of squares
+// needs shuffles (with 8 neighbouring values per lane the other halves' values
+// came by shuffle, and instructions rather than HBM were the bound: 74.4 us for
+// 14000 tokens of 48 heads of 128). The loads of the first batch are in flight
+// while the warp finds the token's sequence, page and angles.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -29,7 +32,7 @@ namespace {
 
 constexpr int QR_THREADS = 256;
 constexpr int QR_WARPS = QR_THREADS / 32;
-constexpr int QR_LOADS = 4;  // 16-byte loads of a batch, per lane
+constexpr int QR_LOADS = 4;  // heads of a batch, per lane
 
 struct RopeFreq {
   double turn[64];  // f_j / (2 pi)
@@ -49,23 +52,18 @@ struct QkArgs {
   int* status;
 };
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+__device__ __forceinline__ void unpack4(const uint2& u, float (&f)[4]) {
+  f[0] = __uint_as_float(u.x << 16);
+  f[1] = __uint_as_float(u.x & 0xffff0000u);
+  f[2] = __uint_as_float(u.y << 16);
+  f[3] = __uint_as_float(u.y & 0xffff0000u);
 }
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&b);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ uint2 pack4(const float (&f)[4]) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
+__device__ __forceinline__ uint2 load4(const bf16* p) { return *reinterpret_cast<const uint2*>(p); }
+__device__ __forceinline__ void store4(bf16* p, const uint2& u) { *reinterpret_cast<uint2*>(p) = u; }
 
 // The sequence that row tok belongs to: the last one that starts at or before it
 // (0 where none does). Each step looks at 32 starts at once.
@@ -102,24 +100,26 @@ __global__ void __launch_bounds__(QR_THREADS, 4)
   }
   if (tok >= a.N) return;
   const int heads = a.q_heads + 2 * c.kv_heads;
-  const int in_head = lane % LANES;          // 8 values of the head
-  const bf16* src = a.qkv + static_cast<long long>(tok) * a.ld + in_head * 8;
+  const int j0 = lane % LANES * 4;           // values j0 .. j0 + 3 of both halves
+  const bf16* src = a.qkv + static_cast<long long>(tok) * a.ld + j0;
   const int step = a.split * BATCH;
   int h0 = part * BATCH + lane / LANES;      // this lane's head of the batch's first load
-  uint4 u[QR_LOADS];
+  uint2 lo[QR_LOADS], hi[QR_LOADS];
   auto fetch = [&](int h) {
 #pragma unroll
-    for (int k = 0; k < QR_LOADS; ++k)
-      if (h + k * HEADS < heads)
-        u[k] = *reinterpret_cast<const uint4*>(src + static_cast<long long>(h + k * HEADS) * D);
-      else
-        u[k] = make_uint4(0u, 0u, 0u, 0u);
+    for (int k = 0; k < QR_LOADS; ++k) {
+      lo[k] = hi[k] = make_uint2(0u, 0u);
+      if (h + k * HEADS < heads) {
+        lo[k] = load4(src + static_cast<long long>(h + k * HEADS) * D);
+        hi[k] = load4(src + static_cast<long long>(h + k * HEADS) * D + D / 2);
+      }
+    }
   };
   fetch(h0);
   const int end = a.offsets[a.B];
   const int pos = a.positions[tok];
-  const uint4 gq = *reinterpret_cast<const uint4*>(a.gamma_q + in_head * 8);
-  const uint4 gk = *reinterpret_cast<const uint4*>(a.gamma_k + in_head * 8);
+  const uint2 gq0 = load4(a.gamma_q + j0), gq1 = load4(a.gamma_q + j0 + D / 2);
+  const uint2 gk0 = load4(a.gamma_k + j0), gk1 = load4(a.gamma_k + j0 + D / 2);
   if (tok >= end) return;                    // behind the last sequence
   // where the token's key and value go: the first value in its page, or -1
   long long row = -1;
@@ -138,8 +138,8 @@ __global__ void __launch_bounds__(QR_THREADS, 4)
     }
     if (row < 0 && lane == 0) atomicOr(a.status, DEV_BAD_CACHE);
   }
-  // angles: lane l reduces those of D/64 rotations, a lane needs the 8 of its values
-  float cs[8], sn[8];
+  // angles: lane l reduces those of D/64 rotations, a lane needs 4
+  float cs[4], sn[4];
   {
     constexpr int PER = D / 64;
     float myc[PER], mys[PER];
@@ -149,50 +149,53 @@ __global__ void __launch_bounds__(QR_THREADS, 4)
       t -= rint(t);
       sincospif(static_cast<float>(2.0 * t), &mys[i], &myc[i]);
     }
-    const int from = (in_head % (LANES / 2)) * (8 / PER);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      cs[i] = __shfl_sync(0xffffffffu, myc[i % PER], from + i / PER);
-      sn[i] = __shfl_sync(0xffffffffu, mys[i % PER], from + i / PER);
-      if (in_head < LANES / 2) sn[i] = -sn[i];  // first half: y_j cos - y_{j+D/2} sin
+    for (int i = 0; i < 4; ++i) {
+      cs[i] = __shfl_sync(0xffffffffu, myc[i % PER], (j0 + i) / PER);
+      sn[i] = __shfl_sync(0xffffffffu, mys[i % PER], (j0 + i) / PER);
     }
   }
   const long long head_stride = static_cast<long long>(c.page_tokens) * D;
+  const int normed = a.q_heads + c.kv_heads;
   const int warp_heads = (heads + HEADS - 1) / HEADS * HEADS;  // the same trips for every lane
   for (; h0 < warp_heads; h0 += step) {
 #pragma unroll
     for (int k = 0; k < QR_LOADS; ++k) {
       const int h = h0 + k * HEADS;
       const bool is_q = h < a.q_heads;
-      uint4 y = u[k];
-      float x[8];
-      unpack8(y, x);
-      float ss = 0.f;
+      uint2 y0 = lo[k], y1 = hi[k];
+      if (h - lane / LANES < normed) {  // the warp holds a q or k head
+        float x0[4], x1[4], g0[4], g1[4];
+        unpack4(y0, x0);
+        unpack4(y1, x1);
+        float ss = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+        for (int i = 0; i < 4; ++i) ss += x0[i] * x0[i] + x1[i] * x1[i];
 #pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float r = 1.f / sqrtf(ss * (1.f / D) + a.eps);
-      float g[8];
-      unpack8(is_q ? gq : gk, g);
+        for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float r = rsqrtf(ss * (1.f / D) + a.eps);
+        unpack4(is_q ? gq0 : gk0, g0);
+        unpack4(is_q ? gq1 : gk1, g1);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] *= r * g[i];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float other = __shfl_xor_sync(0xffffffffu, x[i], LANES / 2);
-        x[i] = x[i] * cs[i] + other * sn[i];
+        for (int i = 0; i < 4; ++i) {
+          const float u = x0[i] * r * g0[i], w = x1[i] * r * g1[i];
+          x0[i] = u * cs[i] - w * sn[i];
+          x1[i] = w * cs[i] + u * sn[i];
+        }
+        if (h < normed) {
+          y0 = pack4(x0);
+          y1 = pack4(x1);
+        }
       }
       if (h >= heads) continue;
-      if (is_q) {
-        *reinterpret_cast<uint4*>(a.q_out + (static_cast<long long>(tok) * a.q_heads + h) * D +
-                                  in_head * 8) = pack8(x);
-      } else if (row >= 0) {
-        const int kv = h - a.q_heads;
-        const bool is_k = kv < c.kv_heads;
-        if (is_k) y = pack8(x);
-        *reinterpret_cast<uint4*>(static_cast<bf16*>(is_k ? c.k : c.v) + row +
-                                  (is_k ? kv : kv - c.kv_heads) * head_stride + in_head * 8) = y;
+      bf16* to = a.q_out + (static_cast<long long>(tok) * a.q_heads + h) * D + j0;
+      if (!is_q) {
+        if (row < 0) continue;
+        to = static_cast<bf16*>(h < normed ? c.k : c.v) + row +
+             (h < normed ? h - a.q_heads : h - normed) * head_stride + j0;
       }
+      store4(to, y0);
+      store4(to + D / 2, y1);
     }
     if (h0 + step < warp_heads) fetch(h0 + step);
   }
