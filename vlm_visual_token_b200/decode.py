@@ -54,55 +54,72 @@ def _declare(L) -> None:
         f.restype, f.argtypes = res, args
 
 
+_ivc = None  # the package, once loaded
+
+
 def _pkg():
-    import vlm_visual_token_b200 as ivc
-    return ivc
+    global _ivc
+    if _ivc is None:
+        import vlm_visual_token_b200 as ivc
+        ivc.lib()
+        _ivc = ivc
+    return _ivc
 
 
 def _refuse(what: str, code: int = -1):
     raise _pkg().IvcError(code, what)
 
 
-def _need(t, what: str, dtype, dims: int, device) -> None:
-    """t is a tensor of this type, rank and device, dense in its last dimension."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != dims or t.device != device:
+def _need(t, what: str, dtype, dims: int, device, n: int = -1) -> int:
+    """t is a dense tensor of this type, rank and device (with n values); its address."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != dims or t.device != device:
         _refuse(f"{what}: a {dims}-dimensional {dtype} tensor on {device} is needed")
-    if t.numel() and not t.is_contiguous():
+    if not t.is_contiguous():
         _refuse(f"{what}: not contiguous")
+    if n >= 0 and t.numel() != n:
+        _refuse(f"{what}: {n} values are needed")
+    return t.data_ptr()
+
+
+def _maybe(t, what: str, dtype, dims: int, device, n: int = -1) -> Optional[int]:
+    return None if t is None else _need(t, what, dtype, dims, device, n)
 
 
 def _rows(t, what: str, dtype, device) -> int:
     """t is a matrix whose rows are dense; the elements between them."""
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != 2 or t.device != device:
         _refuse(f"{what}: a 2-dimensional {dtype} tensor on {device} is needed")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, width = t.shape
+    if width > 1 and t.stride(1) != 1:
         _refuse(f"{what}: rows are not dense")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    return t.stride(0) if rows > 1 else max(width, 1)
 
 
-def _at(t) -> Optional[int]:
-    return None if t is None else t.data_ptr()
-
-
-@contextlib.contextmanager
-def _other(device, stream):
-    with torch.cuda.device(device):
-        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
-            yield
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _on(device, stream):
     """Makes `device` and `stream` current for a call, where they are not."""
     if device.type != "cuda":
-        _refuse("the cache is not on a GPU")
-    if stream is None and device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return _other(device, stream)
+        _refuse("the tensors are not on a GPU")
+    if stream is not None:
+        return _other(device, stream)
+    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+_HERE = contextlib.nullcontext()
+
+
+@contextlib.contextmanager
+def _other(device, stream):
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield
 
 
 def _call(name: str, device, *args) -> None:
     ivc = _pkg()
-    rc = getattr(ivc.lib(), name)(*args, torch.cuda.current_stream(device).cuda_stream)
+    rc = getattr(ivc._LIB, name)(*args, _raw_stream(device.index))
     if rc != 0:
         raise ivc.IvcError(rc, name)
 
@@ -136,9 +153,7 @@ class Cache:
         for name, t, n in (("length", length, seqs), ("n_pages", n_pages, seqs),
                            ("ref", ref, k.shape[1]), ("free_list", free_list, k.shape[1]),
                            ("free_count", free_count, 1)):
-            _need(t, name, torch.int32, 1, dev)
-            if t.numel() != n:
-                _refuse(f"{name}: {n} values are needed")
+            _need(t, name, torch.int32, 1, dev, n)
         self.k, self.v, self.table, self.length, self.n_pages = k, v, table, length, n_pages
         self.ref, self.free_list, self.free_count = ref, free_list, free_count
         self.device = dev
@@ -165,13 +180,6 @@ class Cache:
         return cache
 
 
-def _seqs(cache: Cache, seqs, n: int) -> None:
-    if seqs is not None:
-        _need(seqs, "seqs", torch.int32, 1, cache.device)
-        if seqs.numel() != n:
-            _refuse("seqs: one sequence for each entry is needed")
-
-
 def cache_workspace_size(cache: Cache, n: int, keep_width: int = 0) -> int:
     """Bytes that cache_fork and cache_compact of n sequences need."""
     ivc = _pkg()
@@ -184,29 +192,26 @@ def cache_workspace_size(cache: Cache, n: int, keep_width: int = 0) -> int:
 def cache_reserve(cache: Cache, tokens: torch.Tensor, seqs: Optional[torch.Tensor] = None,
                   workspace=None, stream=None) -> None:
     """Pages for tokens[i] more tokens of sequence seqs[i] (default: i)."""
-    _need(tokens, "tokens", torch.int32, 1, cache.device)
-    n = tokens.numel()
-    _seqs(cache, seqs, n)
-    with _on(cache.device, stream):
-        ws = _workspace(workspace, STEP_WORKSPACE_BYTES, cache.device)
-        _call("ivc_cache_reserve", cache.device, cache._p, tokens.data_ptr(), _at(seqs), n,
-              ws.data_ptr(), ws.numel())
+    dev = cache.device
+    t = _need(tokens, "tokens", torch.int32, 1, dev)
+    n = tokens.shape[0]
+    s = _maybe(seqs, "seqs", torch.int32, 1, dev, n)
+    with _on(dev, stream):
+        ws = _workspace(workspace, STEP_WORKSPACE_BYTES, dev)
+        _call("ivc_cache_reserve", dev, cache._p, t, s, n, ws.data_ptr(), ws.shape[0])
 
 
 def cache_fork(cache: Cache, src: torch.Tensor, dst: torch.Tensor, share: bool = True,
                workspace=None, stream=None) -> None:
     """Empty sequence dst[i] becomes a copy of src[i]: its full pages shared, or
     (share=False) every page copied."""
-    for name, t in (("src", src), ("dst", dst)):
-        _need(t, name, torch.int32, 1, cache.device)
-    n = src.numel()
-    if dst.numel() != n:
-        _refuse("src and dst differ in length")
-    with _on(cache.device, stream):
-        ws = _workspace(workspace, cache_workspace_size(cache, n) if workspace is None else 0,
-                        cache.device)
-        _call("ivc_cache_fork", cache.device, cache._p, src.data_ptr(), dst.data_ptr(), n,
-              1 if share else 0, ws.data_ptr(), ws.numel())
+    dev = cache.device
+    a = _need(src, "src", torch.int32, 1, dev)
+    n = src.shape[0]
+    b = _need(dst, "dst", torch.int32, 1, dev, n)
+    with _on(dev, stream):
+        ws = _workspace(workspace, 0 if workspace is not None else cache_workspace_size(cache, n), dev)
+        _call("ivc_cache_fork", dev, cache._p, a, b, n, 1 if share else 0, ws.data_ptr(), ws.shape[0])
 
 
 def cache_compact(cache: Cache, count: torch.Tensor, keep: Optional[torch.Tensor] = None,
@@ -215,44 +220,40 @@ def cache_compact(cache: Cache, count: torch.Tensor, keep: Optional[torch.Tensor
     """Tokens start[i] + keep[i, j], j < count[i], become tokens start[i] + j, and
     the last of them the sequence's last (keep None: the first count[i]; start
     None: the committed length). Pages behind that are freed."""
-    _need(count, "count", torch.int32, 1, cache.device)
-    n = count.numel()
-    width = 0
+    dev = cache.device
+    m = _need(count, "count", torch.int32, 1, dev)
+    n = count.shape[0]
+    k, width = None, 0
     if keep is not None:
-        _need(keep, "keep", torch.int32, 2, cache.device)
+        k = _need(keep, "keep", torch.int32, 2, dev)
         if keep.shape[0] != n:
             _refuse("keep: one row for each count is needed")
         width = keep.shape[1]
-    if start is not None:
-        _need(start, "start", torch.int32, 1, cache.device)
-        if start.numel() != n:
-            _refuse("start: one value for each count is needed")
-    _seqs(cache, seqs, n)
-    with _on(cache.device, stream):
-        ws = _workspace(workspace, cache_workspace_size(cache, n, width) if workspace is None else 0,
-                        cache.device)
-        # an empty keep has no address: no token can be kept, which count 0 says too
-        _call("ivc_cache_compact", cache.device, cache._p, count.data_ptr(),
-              (_at(keep) or count.data_ptr()) if keep is not None else None, width, _at(start),
-              _at(seqs), n, ws.data_ptr(), ws.numel())
+        k = k or m  # rows of no tokens have no address; none of them is read
+    a = _maybe(start, "start", torch.int32, 1, dev, n)
+    s = _maybe(seqs, "seqs", torch.int32, 1, dev, n)
+    with _on(dev, stream):
+        ws = _workspace(workspace, 0 if workspace is not None else cache_workspace_size(cache, n, width),
+                        dev)
+        _call("ivc_cache_compact", dev, cache._p, m, k, width, a, s, n, ws.data_ptr(), ws.shape[0])
 
 
 def cache_free(cache: Cache, seqs: torch.Tensor, workspace=None, stream=None) -> None:
     """The sequences become empty; pages that no other sequence holds are freed."""
-    _need(seqs, "seqs", torch.int32, 1, cache.device)
-    with _on(cache.device, stream):
-        ws = _workspace(workspace, STEP_WORKSPACE_BYTES, cache.device)
-        _call("ivc_cache_free", cache.device, cache._p, seqs.data_ptr(), seqs.numel(),
-              ws.data_ptr(), ws.numel())
+    dev = cache.device
+    s = _need(seqs, "seqs", torch.int32, 1, dev)
+    with _on(dev, stream):
+        ws = _workspace(workspace, STEP_WORKSPACE_BYTES, dev)
+        _call("ivc_cache_free", dev, cache._p, s, seqs.shape[0], ws.data_ptr(), ws.shape[0])
 
 
-def _batch(offsets, seqs, cache: Cache) -> int:
-    _need(offsets, "offsets", torch.int32, 1, cache.device)
-    B = offsets.numel() - 1
-    if B < 0:
-        _refuse("offsets: at least one value is needed")
-    _seqs(cache, seqs, B)
-    return B
+def _out(out, N: int, q_heads: int, D: int, device):
+    if out is None:
+        return torch.empty(N, q_heads, D, dtype=torch.bfloat16, device=device)
+    _need(out, "out", torch.bfloat16, 3, device)
+    if out.shape != (N, q_heads, D):
+        _refuse("out: [N, q_heads, head_dim] is needed")
+    return out
 
 
 def qk_norm_rope(cache: Cache, layer: int, qkv: torch.Tensor, q_gamma: torch.Tensor,
@@ -269,31 +270,25 @@ def qk_norm_rope(cache: Cache, layer: int, qkv: torch.Tensor, q_gamma: torch.Ten
     q_heads = heads - 2 * cache.kv_heads
     if rest or q_heads < 1:
         _refuse("qkv: q_heads + 2 kv_heads heads of head_dim are needed", -2)
-    for name, t in (("q_gamma", q_gamma), ("k_gamma", k_gamma)):
-        _need(t, name, torch.bfloat16, 1, dev)
-        if t.numel() != D:
-            _refuse(f"{name}: head_dim values are needed")
-    _need(positions, "positions", torch.int32, 1, dev)
-    if positions.numel() != N:
-        _refuse("positions: one for each row is needed")
-    B = _batch(offsets, seqs, cache)
+    gq = _need(q_gamma, "q_gamma", torch.bfloat16, 1, dev, D)
+    gk = _need(k_gamma, "k_gamma", torch.bfloat16, 1, dev, D)
+    pos = _need(positions, "positions", torch.int32, 1, dev, N)
+    off = _need(offsets, "offsets", torch.int32, 1, dev)
+    B = offsets.shape[0] - 1
+    s = _maybe(seqs, "seqs", torch.int32, 1, dev, B)
     with _on(dev, stream):
-        if out is None:
-            out = torch.empty(N, q_heads, D, dtype=torch.bfloat16, device=dev)
-        else:
-            _need(out, "out", torch.bfloat16, 3, dev)
-            if out.shape != (N, q_heads, D):
-                _refuse("out: [N, q_heads, head_dim] is needed")
+        out = _out(out, N, q_heads, D, dev)
         ws = _workspace(workspace, STEP_WORKSPACE_BYTES, dev)
-        _call("ivc_qk_norm_rope", dev, cache._p, layer, qkv.data_ptr(), ld, N, q_heads,
-              q_gamma.data_ptr(), k_gamma.data_ptr(), eps, theta, positions.data_ptr(),
-              offsets.data_ptr(), _at(seqs), B, out.data_ptr(), ws.data_ptr(), ws.numel())
+        _call("ivc_qk_norm_rope", dev, cache._p, layer, qkv.data_ptr(), ld, N, q_heads, gq, gk, eps,
+              theta, pos, off, s, B, out.data_ptr(), ws.data_ptr(), ws.shape[0])
     return out
 
 
 def tree_attention_workspace_size(cache: Cache, N: int, q_heads: int, B: int) -> int:
+    """Bytes that tree_attention needs for N rows of q_heads heads in B sequences."""
     ivc = _pkg()
-    size = ivc.lib().ivc_tree_attention_workspace_size(cache._p, N, q_heads, B)
+    with _on(cache.device, None):
+        size = ivc.lib().ivc_tree_attention_workspace_size(cache._p, N, q_heads, B)
     if size == 0:
         raise ivc.IvcError(-2, "ivc_tree_attention_workspace_size")
     return size
@@ -311,26 +306,20 @@ def tree_attention(cache: Cache, layer: int, q: torch.Tensor, parents: Optional[
             q.device != dev or q.shape[2] != D:
         _refuse(f"q: a bf16 tensor [N, q_heads, {D}] on {dev} is needed")
     N, q_heads, _ = q.shape
-    if q.numel() and (q.stride(2) != 1 or (q_heads > 1 and q.stride(1) != D)):
+    if N and q_heads and (q.stride(2) != 1 or (q_heads > 1 and q.stride(1) != D)):
         _refuse("q: a token's heads are not dense")
     ld = q.stride(0) if N > 1 else q_heads * D
-    if parents is not None:
-        _need(parents, "parents", torch.int32, 1, dev)
-        if parents.numel() != N:
-            _refuse("parents: one for each row is needed")
-    B = _batch(offsets, seqs, cache)
+    par = _maybe(parents, "parents", torch.int32, 1, dev, N)
+    off = _need(offsets, "offsets", torch.int32, 1, dev)
+    B = offsets.shape[0] - 1
+    s = _maybe(seqs, "seqs", torch.int32, 1, dev, B)
     with _on(dev, stream):
-        if out is None:
-            out = torch.empty(N, q_heads, D, dtype=torch.bfloat16, device=dev)
-        else:
-            _need(out, "out", torch.bfloat16, 3, dev)
-            if out.shape != (N, q_heads, D):
-                _refuse("out: [N, q_heads, head_dim] is needed")
-        ws = _workspace(workspace, tree_attention_workspace_size(cache, N, q_heads, B)
-                        if workspace is None else 0, dev)
+        out = _out(out, N, q_heads, D, dev)
+        ws = _workspace(workspace, 0 if workspace is not None else
+                        tree_attention_workspace_size(cache, N, q_heads, B), dev)
         _call("ivc_tree_attention", dev, cache._p, layer, q.data_ptr(), ld, N, q_heads,
-              D ** -0.5 if scale is None else scale, _at(parents), offsets.data_ptr(), _at(seqs), B,
-              out.data_ptr(), ws.data_ptr(), ws.numel())
+              D ** -0.5 if scale is None else scale, par, off, s, B, out.data_ptr(), ws.data_ptr(),
+              ws.shape[0])
     return out
 
 
@@ -344,36 +333,29 @@ def verify_drafts(p: torch.Tensor, q: Optional[torch.Tensor], tokens: torch.Tens
     dev = p.device
     p_ld = _rows(p, "p", torch.float32, dev)
     N, V = p.shape
-    q_ld = 0
+    q_ld, q_at = 0, None
     if q is not None:
-        q_ld = _rows(q, "q", torch.float32, dev)
+        q_ld, q_at = _rows(q, "q", torch.float32, dev), q.data_ptr()
         if q.shape != p.shape:
             _refuse("p and q differ in shape")
-    for name, t, dtype in (("tokens", tokens, torch.int32), ("parents", parents, torch.int32),
-                           ("u", u, torch.float32)):
-        if t is None and name == "parents":
-            continue
-        _need(t, name, dtype, 1, dev)
-        if t.numel() != N:
-            _refuse(f"{name}: one for each row is needed")
-    _need(offsets, "offsets", torch.int32, 1, dev)
-    _need(u_next, "u_next", torch.float32, 1, dev)
-    B = offsets.numel() - 1
-    if B < 0 or u_next.numel() != B:
-        _refuse("u_next: one for each sequence is needed")
+    tok = _need(tokens, "tokens", torch.int32, 1, dev, N)
+    par = _maybe(parents, "parents", torch.int32, 1, dev, N)
+    uu = _need(u, "u", torch.float32, 1, dev, N)
+    off = _need(offsets, "offsets", torch.int32, 1, dev)
+    B = offsets.shape[0] - 1
+    un = _need(u_next, "u_next", torch.float32, 1, dev, max(B, 0))
     with _on(dev, stream):
         if out is None:
-            out = (torch.empty(B, path_width, dtype=torch.int32, device=dev),
-                   torch.empty(B, dtype=torch.int32, device=dev),
-                   torch.empty(B, dtype=torch.int32, device=dev))
+            out = (torch.empty(max(B, 0), path_width, dtype=torch.int32, device=dev),
+                   torch.empty(max(B, 0), dtype=torch.int32, device=dev),
+                   torch.empty(max(B, 0), dtype=torch.int32, device=dev))
         path, n_path, token = out
-        _need(path, "path", torch.int32, 2, dev)
-        for name, t in (("n_path", n_path), ("next_token", token)):
-            _need(t, name, torch.int32, 1, dev)
-            if t.numel() != B or path.shape[0] != B:
-                _refuse("out: one entry for each sequence is needed")
+        at = _need(path, "path", torch.int32, 2, dev)
+        if path.shape[0] != B:
+            _refuse("path: one row for each sequence is needed")
+        m, t = _need(n_path, "n_path", torch.int32, 1, dev, B), _need(token, "next_token", torch.int32, 1,
+                                                                    dev, B)
         ws = _workspace(workspace, STEP_WORKSPACE_BYTES, dev)
-        _call("ivc_verify_drafts", dev, p.data_ptr(), p_ld, _at(q), q_ld, N, V, tokens.data_ptr(),
-              _at(parents), offsets.data_ptr(), B, u.data_ptr(), u_next.data_ptr(), path.data_ptr(),
-              path.shape[1], n_path.data_ptr(), token.data_ptr(), ws.data_ptr(), ws.numel())
+        _call("ivc_verify_drafts", dev, p.data_ptr(), p_ld, q_at, q_ld, N, V, tok, par, off, B, uu, un,
+              at, path.shape[1], m, t, ws.data_ptr(), ws.shape[0])
     return out
