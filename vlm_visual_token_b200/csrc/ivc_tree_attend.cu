@@ -3,7 +3,7 @@
 //
 // out_i = sum_j softmax_j(scale q_i . k_j) v_j over the committed tokens, the
 // node's ancestors and the node itself. One pass with the running maximum m and
-// sum l: per tile of 128 keys p = e^(s - m), l = sum p, o = sum p v, all rescaled
+// sum l: per tile of 64 keys p = e^(s - m), l = sum p, o = sum p v, all rescaled
 // by e^(m - m') when the maximum rises to m'; out = o / l.
 //
 // What bounds it: a (sequence, kv head)'s keys and values are read from HBM once
@@ -19,11 +19,15 @@
 //     unit busy at the same time: with more than 128 query rows each group has
 //     128 rows and every tile; with fewer (plain decoding) both have the same
 //     rows and every other tile, and the groups' results are merged at the end.
-// Per group and tile: S[128 rows x 128 keys] = Q K^T (M 128, N 128), S read from
+// Per group and tile: S[128 rows x 64 keys] = Q K^T (M 128, N 64), S read from
 // TMEM (thread = row), p written back over S as bf16 and used as the A operand of
-// O[128 x D] += P V (V read MN-major). O stays in TMEM; it is rescaled only when a
-// row's maximum rose by more than 2^8 (p then reaches 2^8 at most, which bf16 and
-// the fp32 sums hold as exactly as values below 1).
+// O[128 x D] += P V (V read MN-major). A group has two S buffers, so that the
+// scores of its next tile are made while it works on this one: with one buffer of
+// 128 keys the scores had to wait for the weighted sum (P lies in S), each group
+// idled half of the time, and 64 nodes x 4 sequences of up to 40800 tokens took
+// 237 us. O stays in TMEM; it is rescaled only when a row's maximum rose by more
+// than 2^8 (p then reaches 2^8 at most, which bf16 and the fp32 sums hold as
+// exactly as values below 1).
 //
 // Rounding: p to bf16 for the product with v (the sum l takes the unrounded p);
 // everything else is fp32 until the output.
@@ -34,9 +38,12 @@
 // tokens by 0 in shared memory (0 x inf would reach every row); rows that do see
 // such a token get the non-finite value back in the epilogue.
 //
-// Warp 8 loads, warp 9 issues the MMAs from one thread, warp 10 mends value tiles,
-// warps 0-3 and 4-7 are the softmax groups. Every wait is bounded
-// (IVC_DEV_WAIT_TIMEOUT).
+// Warp 8 loads, warps 9 and 10 issue the MMAs of one group each, warp 11 mends value
+// tiles, warps 0-3 and 4-7 are the softmax groups. Two issuing warps, because an
+// MMA's issue takes as long as the MMA and a barrier wait 150 to 350 cycles even
+// when it is over: with one warp the waits of each 64-key step (about 1000 cycles)
+// added to its MMAs (760), now they pass behind the other group's MMAs. Every wait
+// is bounded (IVC_DEV_WAIT_TIMEOUT).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -46,10 +53,11 @@
 namespace ivc {
 namespace {
 
-constexpr int TA_THREADS = 352;
-constexpr int TA_KEYS = 128;                 // keys of a tile
+constexpr int TA_THREADS = 384;
+constexpr int TA_KEYS = 64;                  // keys of a tile
 constexpr int TA_ROWS = 128;                 // query rows of a group
-constexpr uint32_t TA_HALF = 128 * 128;      // 128 rows x 64 values
+constexpr uint32_t TA_QHALF = 128 * 128;     // 128 query rows x 64 values
+constexpr uint32_t TA_HALF = TA_KEYS * 128;  // a tile's keys x 64 values
 constexpr int TA_MAX_BATCH = 4096;
 constexpr int TA_MAX_GRID = 256;              // CTAs, one per SM
 constexpr float TA_RISE = 8.f;               // log2 of the rise of m that rescales
@@ -191,6 +199,33 @@ struct Walk {
 };
 
 // ------------------------------------------------------------------ tcgen05 pieces
+// A bounded wait of a whole warp: every lane gets the same answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+// Whether the phase is over, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+// One lane of a converged warp, always the same. The compiler knows that a branch
+// on it is taken by one lane, which a branch on the lane number hides from it.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 // D[tmem] (+)= A[tmem, bf16 pairs] * B[smem desc].
 __device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                              uint32_t idesc, uint32_t accumulate) {
@@ -231,26 +266,32 @@ struct TaSmem {
   static constexpr int HALVES = D / 64;
   static constexpr uint32_t SLOT = HALVES * TA_HALF;    // one tile of keys or values
   static constexpr int SLOTS = 163840 / SLOT;           // 160 KB
-  static constexpr uint32_t Q = 2 * HALVES * TA_HALF;   // two groups' rows
+  static constexpr uint32_t Q = 2 * HALVES * TA_QHALF;  // two groups' rows
   static constexpr uint32_t TOTAL = 1024 + Q + SLOTS * SLOT;
 };
 
-// The keys that row `node` sees in tile t0 as bits: committed tokens, and the
-// node's ancestors and itself (anc) behind them.
+// The keys that a node sees in the tile at t0 as bits: committed tokens, and
+// behind them the node's ancestors and itself (anc).
 __device__ __forceinline__ void tile_mask(const uint32_t (&anc)[4], int len, int t0,
-                                          uint32_t (&mask)[4]) {
+                                          uint32_t (&mask)[2]) {
   const int shift = len - t0;  // tile position of node 0
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < 2; ++w) {
     const int below = shift - 32 * w;  // committed tokens in this word
     uint32_t m = below >= 32 ? 0xffffffffu : below <= 0 ? 0u : (1u << below) - 1u;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const int s = shift + 32 * x - 32 * w;  // anc word x starts at bit s of this word
+      const int s = below + 32 * x;  // anc word x starts at bit s of this word
       if (s > -32 && s < 32) m |= s >= 0 ? anc[x] << s : anc[x] >> -s;
     }
     mask[w] = m;
   }
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 template <int D>
@@ -266,28 +307,32 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
   uint8_t* sq = sm;
   uint8_t* ring = sm + S::Q;
   __shared__ __align__(8) uint64_t full[S::SLOTS], empty[S::SLOTS];
-  __shared__ __align__(8) uint64_t qfull, qempty, sfull[2], pready[2], ofull, ofree, mlready;
-  __shared__ __align__(8) uint64_t mend, mended;
+  __shared__ __align__(8) uint64_t sfull[2][2], pready[2][2], odone[2];  // [group][S buffer]
+  __shared__ __align__(8) uint64_t qfull, qempty, ofull, ofree, mlready;
+  __shared__ __align__(8) uint64_t mend[2], mended[2];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_mend_slot, s_mend_tile, s_odd[2];  // s_odd: a drafted value is not finite
+  __shared__ int s_mend_slot[2], s_odd[2];  // s_odd: a drafted value is not finite
   __shared__ float2 s_ml[TA_ROWS];                    // group 1's maximum and sum
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::SLOTS; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 2);  // both issuers
     }
     mbar_init(&qfull, 1);
-    mbar_init(&qempty, 1);
+    mbar_init(&qempty, 2);
     for (int g = 0; g < 2; ++g) {
-      mbar_init(&sfull[g], 1);
-      mbar_init(&pready[g], 4);
+      for (int buf = 0; buf < 2; ++buf) {
+        mbar_init(&sfull[g][buf], 1);
+        mbar_init(&pready[g][buf], 4);
+      }
+      mbar_init(&odone[g], 1);
+      mbar_init(&mend[g], 1);
+      mbar_init(&mended[g], 1);
     }
-    mbar_init(&ofull, 1);
+    mbar_init(&ofull, 2);
     mbar_init(&ofree, 8);
     mbar_init(&mlready, 4);
-    mbar_init(&mend, 1);
-    mbar_init(&mended, 1);
     s_odd[0] = s_odd[1] = 0;
     fence_mbar_init();
     tma_prefetch_desc(&qmap);
@@ -301,50 +346,75 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  // all 512 columns were asked for, so the base is 0; as a constant it spares the
+  // MMAs a register each
+  constexpr uint32_t tmem = 0;
   bool ok = true;
   pdl_wait();     // the plan; everything before it in the stream
   pdl_trigger();  // the merge may launch; it waits for this grid
 
   if (warp == 8) {
     // ------------------------------------------------------------- producer
-    const int pt = c.page_tokens, per_tile = TA_KEYS / pt;
-    const long long nowhere = static_cast<long long>(c.pages) * c.kv_heads * pt;  // reads as 0
+    const int pt = c.page_tokens, box = min(pt, TA_KEYS), per_tile = TA_KEYS / box;
+    const int pt_log = 31 - __clz(pt), box_log = 31 - __clz(box);
+    const int nowhere = c.pages * c.kv_heads * pt;  // behind the last row: reads as 0
     Walk walk(a);
     Item it = {};
-    int loads = 0, items = 0, queries = 0;
-    // one tile of keys or values: lane i has the i-th page of the tile
-    auto load = [&](const CUtensorMap* map, int tile) {
-      const int s = loads % S::SLOTS;
-      if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ((loads / S::SLOTS) & 1) ^ 1))) return false;
-      if (lane == 0) mbar_arrive_expect_tx(&full[s], S::SLOT);
-      __syncwarp();
-      if (lane < per_tile) {
-        const int at = tile * per_tile + lane;
-        long long row = nowhere;
-        if (at < div_up(it.len + it.n, pt)) {
-          const int page = c.table[static_cast<size_t>(it.seq) * c.max_pages + at];
-          if (page >= 0 && page < c.pages)
-            row = (static_cast<long long>(page) * c.kv_heads + it.h) * pt;
-          else
-            atomicOr(a.status, DEV_BAD_CACHE);
-        }
-        uint8_t* dst = ring + s * S::SLOT + lane * pt * 128;
-#pragma unroll
-        for (int hf = 0; hf < S::HALVES; ++hf)
-          tma_load_2d(dst + hf * TA_HALF, map, &full[s], 64 * hf, static_cast<int>(row));
+    int slot = 0, round = 0, queries = 0, items = 0;
+    // Rows of the boxes (a page or half of one) of an item: lane l holds those of
+    // boxes base + l and base + 32 + l, so that the table is read 32 boxes ahead.
+    struct Rows {
+      int base, now, next;
+    };
+    auto row_of = [&](int b) -> int {
+      const int token = b << box_log;
+      if (token >= it.len + it.n) return nowhere;
+      const int page = c.table[static_cast<size_t>(it.seq) * c.max_pages + (token >> pt_log)];
+      if (page < 0 || page >= c.pages) {
+        atomicOr(a.status, DEV_BAD_CACHE);
+        return nowhere;
       }
-      ++loads;
+      return (page * c.kv_heads + it.h) * pt + (token & (pt - 1));
+    };
+    auto begin = [&](Rows& r) {
+      r.base = it.t0 * per_tile & ~31;
+      r.now = row_of(r.base + lane);
+      r.next = row_of(r.base + 32 + lane);
+    };
+    // one tile of keys or values
+    auto load = [&](const CUtensorMap* map, Rows& r, int tile) {
+      const int first = tile * per_tile;
+      if (first >= r.base + 32) {
+        r.base += 32;
+        r.now = r.next;
+        r.next = row_of(r.base + 32 + lane);
+      }
+      if (!warp_wait(&empty[slot], (round & 1) ^ 1)) return false;
+      uint8_t* dst = ring + slot * S::SLOT;
+      if (elect_one()) mbar_arrive_expect_tx(&full[slot], S::SLOT);
+      for (int i = 0; i < per_tile; ++i) {
+        const int row = __shfl_sync(0xffffffffu, r.now, (first + i) & 31);
+        if (elect_one()) {
+#pragma unroll
+          for (int hf = 0; hf < S::HALVES; ++hf)
+            tma_load_2d(dst + hf * TA_HALF + i * box * 128, map, &full[slot], 64 * hf, row);
+        }
+      }
+      __syncwarp();
+      if (++slot == S::SLOTS) {
+        slot = 0;
+        ++round;
+      }
       return true;
     };
     auto load_q = [&]() {
-      if (!__all_sync(0xffffffffu, mbar_wait(&qempty, (items & 1) ^ 1))) return false;
+      if (!warp_wait(&qempty, (items & 1) ^ 1)) return false;
       if (lane == 0) {
         const int tiles = it.rows2 ? 2 : 1;
         mbar_arrive_expect_tx(&qfull, tiles * S::HALVES * a.npt * a.group * 128);
         for (int g = 0; g < tiles; ++g)
           for (int hf = 0; hf < S::HALVES; ++hf)
-            tma_load_3d(sq + (g * S::HALVES + hf) * TA_HALF, &qmap, &qfull, 64 * hf,
+            tma_load_3d(sq + (g * S::HALVES + hf) * TA_QHALF, &qmap, &qfull, 64 * hf,
                         it.h * a.group, it.row + it.node0 + g * a.npt);
       }
       ++queries;
@@ -354,107 +424,168 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
     while (ok && walk.next(c, a, it)) {
       // in the order in which the MMAs first use them (see there); the queries,
       // whose buffer the item before holds longest, after the first keys
-      const int ahead = it.rows2 ? 1 : 2, T = it.t1 - it.t0;
-      for (int t = 0; t < ahead && t < T && ok; ++t) ok = load(&kmap, it.t0 + t);
+      const int ahead = it.rows2 ? 2 : 4, T = it.t1 - it.t0;
+      Rows krows, vrows;
+      begin(krows);
+      vrows = krows;
+      for (int t = 0; t < ahead && t < T && ok; ++t) ok = load(&kmap, krows, it.t0 + t);
       if (ok) ok = load_q();
       for (int t = 0; t < T && ok; ++t) {
-        ok = load(&vmap, it.t0 + t);
-        if (ok && t + ahead < T) ok = load(&kmap, it.t0 + t + ahead);
+        ok = load(&vmap, vrows, it.t0 + t);
+        if (ok && t + ahead < T) ok = load(&kmap, krows, it.t0 + t + ahead);
       }
       ++items;
     }
     if (!ok) {  // let the copies in flight land
+      const int loads = round * S::SLOTS + slot;
       for (int i = max(0, loads - S::SLOTS); i < loads; ++i)
         mbar_wait(&full[i % S::SLOTS], (i / S::SLOTS) & 1);
       if (queries > 0) mbar_wait(&qfull, (queries - 1) & 1);
     }
-  } else if (warp == 9) {
-    if (lane == 0) {
-      // ----------------------------------------------------------- MMA issuer
-      // unit u: group u & 1, tile u / 2 (own rows) or u (own tiles). Scores of
-      // unit u + 2 follow the weighted sum of unit u, whose weights lie in the
-      // same columns.
-      const uint32_t idesc_s = idesc_bf16_f32(128, TA_KEYS);
-      const uint32_t idesc_o = idesc_bf16_f32(128, D) | (1u << 16);  // B MN-major
-      Walk walk(a);
-      Item it = {};
-      int loads = 0, items = 0, mends = 0;
-      int np[2] = {0, 0};                    // weights consumed per group
-      while (ok && walk.next(c, a, it)) {
-        const int U = it.units();
-        int kslot = 0, vslot = 0;
-        s_odd[items & 1] = 0;
-        auto take = [&](int& slot) {         // the next load in order
-          slot = loads % S::SLOTS;
-          const bool r = mbar_wait(&full[slot], (loads / S::SLOTS) & 1);
-          ++loads;
-          return r;
-        };
-        auto scores = [&](int u) {
-          const int g = u & 1;
-          if (!it.rows2 || g == 0)
-            if (!take(kslot)) return false;
-          if (u == 0 && !mbar_wait(&qfull, items & 1)) return false;
-          tc_fence_after();
-          const uint32_t qa = smem_u32(sq + (it.rows2 ? g : 0) * S::HALVES * TA_HALF);
-          const uint32_t ka = smem_u32(ring + kslot * S::SLOT);
-#pragma unroll
-          for (int hf = 0; hf < S::HALVES; ++hf) {
-            const uint64_t ad = sw128_kmajor_desc(qa + hf * TA_HALF);
-            const uint64_t bd = sw128_kmajor_desc(ka + hf * TA_HALF);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_bf16(tmem + 128 * g, ad + 2 * kk, bd + 2 * kk, idesc_s, (hf | kk) != 0);
-          }
-          umma_commit(&sfull[g]);
-          if (!it.rows2 || g == 1) umma_commit(&empty[kslot]);
-          if (u == U - 1) umma_commit(&qempty);
-          return true;
-        };
-        ok = scores(0);
-        if (ok && U > 1) ok = scores(1);
-        for (int u = 0; u < U && ok; ++u) {
-          const int g = u & 1, tile = it.t0 + (it.rows2 ? u >> 1 : u);
-          bool mend_it = false;
-          if (!it.rows2 || g == 0) {
-            if (!take(vslot)) { ok = false; break; }
-            mend_it = (tile + 1) * TA_KEYS > it.len;  // reaches behind the committed tokens
-            if (mend_it) {
-              s_mend_slot = vslot;
-              s_mend_tile = tile;
-              mbar_arrive(&mend);
-            }
-          }
-          if (!mbar_wait(&pready[g], np[g]++ & 1)) { ok = false; break; }
-          if (mend_it && !mbar_wait(&mended, mends++ & 1)) { ok = false; break; }
-          if (u == 0 && !mbar_wait(&ofree, (items & 1) ^ 1)) { ok = false; break; }
-          tc_fence_after();
-          const uint64_t bd =
-              sw128_mnmajor_desc(smem_u32(ring + vslot * S::SLOT), TA_HALF);
-#pragma unroll
-          for (int kk = 0; kk < TA_KEYS / 16; ++kk)
-            umma_bf16_ta(tmem + 256 + 128 * g, tmem + 128 * g + 8 * kk,
-                         bd + ((2048 * kk) >> 4), idesc_o, (u >= 2 || kk != 0) ? 1u : 0u);
-          if (!it.rows2 || g == 1) umma_commit(&empty[vslot]);
-          if (u == U - 1) umma_commit(&ofull);
-          if (u + 2 < U) ok = scores(u + 2);
+  } else if (warp == 9 || warp == 10) {
+    // ------------------------------------------------------------- MMA issuers
+    // unit u: group u & 1, tile u / 2 (own rows) or u (own tiles), S buffer
+    // u / 2 & 1. Scores of unit u + 4 follow the weighted sum of unit u, whose
+    // weights lie in the same columns. Each warp issues its group's units, but
+    // takes every load in turn (a barrier's phases cannot be skipped) and, where
+    // a tile is not its own, gives it back at once.
+    const int g = warp - 9;
+    const uint32_t idesc_s = idesc_bf16_f32(128, TA_KEYS);
+    const uint32_t idesc_o = idesc_bf16_f32(128, D) | (1u << 16);  // B MN-major
+    const uint64_t kdesc = sw128_kmajor_desc(smem_u32(ring));
+    const uint64_t vdesc = sw128_mnmajor_desc(smem_u32(ring), TA_HALF);
+    Walk walk(a);
+    Item it = {};
+    int items = 0, mends = 0;
+    int slot = 0, round = 0;               // of the next load in order
+    uint32_t np = 0;                       // bit buffer: phase of the weights
+    while (ok && walk.next(c, a, it)) {
+      const int U = it.units(), mine = (U + 1 - g) / 2;
+      const bool all = it.rows2;           // every tile is used by both groups
+      const uint64_t qdesc = sw128_kmajor_desc(smem_u32(sq) + (all ? g : 0) * S::HALVES * TA_QHALF);
+      const int T = it.t1 - it.t0, ahead = all ? 2 : 4;
+      struct Load {                        // a load in order: its slot and phase
+        int slot;
+        uint32_t parity;
+      };
+      auto next_load = [&]() {
+        const Load x{slot, static_cast<uint32_t>(round & 1)};
+        if (++slot == S::SLOTS) {
+          slot = 0;
+          ++round;
         }
-        ++items;
+        return x;
+      };
+      auto own = [&](int t) { return all || (t & 1) == g; };
+      // by one lane: this group's scores with the keys of its unit i ...
+      auto issue_scores = [&](int ks, int i) {
+        const uint64_t bd = kdesc + (ks * S::SLOT >> 4);
+        const int buf = i & 1;
+#pragma unroll
+        for (int hf = 0; hf < S::HALVES; ++hf)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16(tmem + 128 * g + 64 * buf, qdesc + (hf * TA_QHALF >> 4) + 2 * kk,
+                      bd + (hf * TA_HALF >> 4) + 2 * kk, idesc_s, (hf | kk) != 0);
+        umma_commit(&sfull[g][buf]);
+        umma_commit(&empty[ks]);
+        if (i == mine - 1) umma_commit(&qempty);
+      };
+      // ... and its weighted sum of the values of unit i
+      auto issue_sum = [&](int vs, int i) {
+        const uint64_t bd = vdesc + (vs * S::SLOT >> 4);
+        const int buf = i & 1;
+#pragma unroll
+        for (int kk = 0; kk < TA_KEYS / 16; ++kk)
+          umma_bf16_ta(tmem + 256 + 128 * g, tmem + 128 * g + 64 * buf + 8 * kk,
+                       bd + ((2048 * kk) >> 4), idesc_o, (i != 0 || kk != 0) ? 1u : 0u);
+        umma_commit(&odone[g]);
+        umma_commit(&empty[vs]);
+        if (i == mine - 1) umma_commit(&ofull);
+      };
+      for (int t = 0; t < ahead && t < T && ok; ++t) {
+        const Load k = next_load();
+        ok = warp_wait(&full[k.slot], k.parity);
+        if (ok && t == 0) ok = warp_wait(&qfull, items & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          if (own(t)) issue_scores(k.slot, all ? t : t >> 1);
+          else mbar_arrive(&empty[k.slot]);
+        }
+        __syncwarp();
       }
+      if (ok && mine == 0) {               // a single tile: nothing for group 1, which
+        ok = warp_wait(&ofree, (items & 1) ^ 1);  // must not count for the item before
+        if (ok && lane == 0) {
+          mbar_arrive(&qempty);
+          mbar_arrive(&ofull);
+        }
+        __syncwarp();
+      }
+      int done = 0;                        // own units summed
+      for (int t = 0; t < T && ok; ++t) {
+        const bool more = t + ahead < T, mine_now = own(t);
+        const Load v = next_load();
+        Load k{0, 0};
+        if (more) k = next_load();
+        const int buf = done & 1, later = all ? t + ahead : (t + ahead) >> 1;
+        const bool mend_it = mine_now && (it.t0 + t + 1) * TA_KEYS > it.len;  // reaches behind
+        if (mend_it) {                                                        // the committed
+          if (!warp_wait(&full[v.slot], v.parity)) { ok = false; break; }
+          if (lane == 0 && (!all || g == 0)) {
+            s_mend_slot[g] = v.slot;
+            mbar_arrive(&mend[g]);
+          }
+        }
+        // the values, the weights and the keys of the scores that follow: one wait
+        // for all three, and one branch with all MMAs of the step
+        long long since = 0;
+        while (!__all_sync(0xffffffffu,
+                           mbar_test(&full[v.slot], v.parity) &&
+                               (!more || mbar_test(&full[k.slot], k.parity)) &&
+                               (!mine_now || mbar_test(&pready[g][buf], (np >> buf) & 1)))) {
+          const long long now = clock64();
+          if (since == 0) since = now;
+          if (__any_sync(0xffffffffu, now - since > IVC_WAIT_CYCLES)) { ok = false; break; }
+        }
+        if (ok && mend_it) ok = warp_wait(&mended[g], mends++ & 1);
+        if (ok && mine_now && done == 0) ok = warp_wait(&ofree, (items & 1) ^ 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          if (mine_now) {
+            issue_sum(v.slot, done);
+            if (more) issue_scores(k.slot, later);
+          } else {
+            mbar_arrive(&empty[v.slot]);
+            if (more) mbar_arrive(&empty[k.slot]);
+          }
+        }
+        __syncwarp();
+        if (mine_now) {
+          np ^= 1u << buf;
+          ++done;
+        }
+      }
+      ++items;
     }
-    __syncwarp();
-  } else if (warp == 10) {
+  } else if (warp == 11) {
     // ------------------------------------------------- value tiles at the end
     Walk walk(a);
     Item it = {};
-    int mends = 0, items = 0;
+    int mends[2] = {0, 0}, items = 0;
     while (ok && walk.next(c, a, it)) {
-      for (int tile = max(it.t0, it.len / TA_KEYS); tile < it.t1 && ok; ++tile) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&mend, mends & 1));
+      const int first = max(it.t0, it.len / TA_KEYS);
+      for (int tile = first; tile < it.t1 && ok; ++tile) {
+        const int g = it.rows2 ? 0 : (tile - it.t0) & 1;  // the issuer that asks
+        ok = warp_wait(&mend[g], mends[g]++ & 1);
         if (!ok) break;
-        ++mends;
-        uint8_t* v = ring + s_mend_slot * S::SLOT;
-        const int base = s_mend_tile * TA_KEYS;
+        // (no epilogue reads the flag of two items before any more)
+        if (tile == first && lane == 0) s_odd[items & 1] = 0;
+        __syncwarp();
+        uint8_t* v = ring + s_mend_slot[g] * S::SLOT;
+        const int base = tile * TA_KEYS;
         const int drafted = max(0, it.len - base);                    // first drafted row
         const int behind = min(TA_KEYS, it.len + it.n - base);       // first row behind them
         const int pages_end = min(TA_KEYS, div_up(it.len + it.n, c.page_tokens) * c.page_tokens - base);
@@ -486,7 +617,10 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
         if (odd) s_odd[items & 1] = 1;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(&mended);
+        if (lane == 0) {
+          mbar_arrive(&mended[g]);
+          if (it.rows2) mbar_arrive(&mended[1]);
+        }
       }
       ++items;
     }
@@ -495,11 +629,12 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
     const int g = warp >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;                   // row of the group = TMEM lane
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t ts = tmem + lanes + 128 * g, to = tmem + lanes + 256 + 128 * g;
+    const uint32_t to = tmem + lanes + 256 + 128 * g;
     const int first_lane_row = quad * 32;
     Walk walk(a);
     Item it = {};
-    int items = 0, ns = 0, nml = 0;
+    int items = 0, nml = 0, sums = 0;  // sums: weighted sums asked for by this group
+    uint32_t ns = 0;                   // bit buffer: phase of the scores
     while (ok && walk.next(c, a, it)) {
       const int U = it.units();
       const int node0 = it.node0 + (it.rows2 ? g * a.npt : 0);        // of the group
@@ -536,48 +671,42 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
       }
       float m = -INFINITY, l = 0.f;   // the maximum that p is taken against, in log2 units
       for (int u = g; u < U && ok; u += 2) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&sfull[g], ns & 1));
+        const int buf = (u >> 1) & 1;
+        const uint32_t ts = tmem + lanes + 128 * g + 64 * buf;
+        ok = warp_wait(&sfull[g][buf], (ns >> buf) & 1);
         if (!ok) break;
-        ++ns;
+        ns ^= 1u << buf;
         tc_fence_after();
         if (live) {
           const int tile = it.t0 + (it.rows2 ? u >> 1 : u);
-          const bool masked = (tile + 1) * TA_KEYS > it.len;
-          uint32_t mask[4] = {~0u, ~0u, ~0u, ~0u};
-          if (masked) tile_mask(anc, it.len, tile * TA_KEYS, mask);
           uint32_t x0[32], x1[32];
-          float top = -INFINITY;
-          auto biggest = [&](uint32_t (&x)[32], uint32_t keep) {
-            if (masked) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!((keep >> j) & 1)) x[j] = 0xff800000u;  // -inf
-            }
-            float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              t0 = fmaxf(t0, __uint_as_float(x[j]));
-              t1 = fmaxf(t1, __uint_as_float(x[j + 1]));
-            }
-            top = fmaxf(top, fmaxf(t0, t1));
-          };
-          // the second half of the keys first: the weights of the first half
-          // then overwrite scores that are in registers
-          tmem_ld32(ts + 64, x0);
-          tmem_ld32(ts + 96, x1);
-          tmem_ld_wait();
-          biggest(x0, mask[2]);
-          biggest(x1, mask[3]);
           tmem_ld32(ts, x0);
           tmem_ld32(ts + 32, x1);
           tmem_ld_wait();
-          biggest(x0, mask[0]);
-          biggest(x1, mask[1]);
-          const float rise = top * a.scale_log2;
+          if ((tile + 1) * TA_KEYS > it.len) {
+            uint32_t mask[2];
+            tile_mask(anc, it.len, tile * TA_KEYS, mask);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              if (!((mask[0] >> j) & 1)) x0[j] = 0xff800000u;  // -inf
+              if (!((mask[1] >> j) & 1)) x1[j] = 0xff800000u;
+            }
+          }
+          float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            t0 = max3(t0, __uint_as_float(x0[j]), __uint_as_float(x0[j + 1]));
+            t1 = max3(t1, __uint_as_float(x1[j]), __uint_as_float(x1[j + 1]));
+          }
+          const float rise = fmaxf(t0, t1) * a.scale_log2;
           if (u < 2) {
             m = rise;
           } else if (__any_sync(0xffffffffu, rise - m > TA_RISE)) {
-            // every earlier sum of this group is complete: its scores followed it
+            // once this group's sum before is complete (the one before that is:
+            // these scores lie in the columns of its weights)
+            ok = warp_wait(&odone[g], (sums - 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
             const float m2 = fmaxf(m, rise);
             const float f = m2 == -INFINITY ? 1.f : ex2(m - m2);
             m = m2;
@@ -595,42 +724,29 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
           const float base = m == -INFINITY ? 0.f : m;
           float sum0 = 0.f, sum1 = 0.f;
           uint32_t p[32];
-          auto weights = [&](const uint32_t (&x)[32], int first) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float e0 = ex2(fmaf(__uint_as_float(x[j]), a.scale_log2, -base));
-              const float e1 = ex2(fmaf(__uint_as_float(x[j + 1]), a.scale_log2, -base));
-              sum0 += e0;
-              sum1 += e1;
-              p[first + j / 2] = pack_bf16(e0, e1);
-            }
-          };
-          weights(x0, 0);
-          weights(x1, 16);
-          tmem_st32(ts, p);
-          tmem_ld32(ts + 64, x0);
-          tmem_ld32(ts + 96, x1);
-          tmem_ld_wait();
-          if (masked) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              if (!((mask[2] >> j) & 1)) x0[j] = 0xff800000u;
-              if (!((mask[3] >> j) & 1)) x1[j] = 0xff800000u;
-            }
+          for (int j = 0; j < 32; j += 2) {
+            const float e0 = ex2(fmaf(__uint_as_float(x0[j]), a.scale_log2, -base));
+            const float e1 = ex2(fmaf(__uint_as_float(x0[j + 1]), a.scale_log2, -base));
+            const float e2 = ex2(fmaf(__uint_as_float(x1[j]), a.scale_log2, -base));
+            const float e3 = ex2(fmaf(__uint_as_float(x1[j + 1]), a.scale_log2, -base));
+            sum0 += e0 + e1;
+            sum1 += e2 + e3;
+            p[j / 2] = pack_bf16(e0, e1);
+            p[16 + j / 2] = pack_bf16(e2, e3);
           }
-          weights(x0, 0);
-          weights(x1, 16);
-          tmem_st32(ts + 32, p);
+          tmem_st32(ts, p);
           l += sum0 + sum1;
           tmem_st_wait();
         }
+        ++sums;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pready[g]);
+        if (lane == 0) mbar_arrive(&pready[g][buf]);
       }
       // ---------------------------------------------------------- epilogue
       const bool two = !it.rows2 && U > 1;  // both groups have sums of the same rows
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(&ofull, items & 1));
+      ok = ok && warp_wait(&ofull, items & 1);
       if (!ok) break;
       if (!it.rows2 && g == 1) {  // group 0 merges and writes
         if (two) {
@@ -642,7 +758,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
         ++items;
         continue;
       }
-      if (two) ok = __all_sync(0xffffffffu, mbar_wait(&mlready, nml++ & 1));
+      if (two) ok = warp_wait(&mlready, nml++ & 1);
       if (!ok) break;
       tc_fence_after();
       if (live) {
@@ -665,7 +781,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
         bf16* dst = a.out + (static_cast<long long>(it.row + node) * a.q_heads +
                              it.h * a.group + r % a.group) * D;
         float* part = a.part_o + (static_cast<size_t>(slot) * 256 + prow) * D;
-        const bool odd = s_odd[items & 1] != 0;
+        const bool odd = it.t1 * TA_KEYS > it.len && s_odd[items & 1] != 0;
 #pragma unroll 1
         for (int d = 0; d < D; d += 32) {
           __syncwarp();
@@ -739,7 +855,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
   __syncthreads();
   if (warp == 9) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(s_tmem, 512);
   }
 }
 
@@ -766,7 +882,7 @@ __global__ void __launch_bounds__(256)
   {
     const long long total = a.prefix[a.B];
     const long long item_end = total * (i + 1) / grid + h1.z;
-    for (int j = i + 1 + threadIdx.x; j < grid; j += 256) {
+    for (int j = i + 1 + threadIdx.x; j < grid; j += blockDim.x) {
       const long long pos = total * j / grid;
       if (pos >= item_end) break;
       s_slot[j - i] = pos < total * (j + 1) / grid ? 2 * j : -1;  // -1: an empty piece
@@ -777,7 +893,7 @@ __global__ void __launch_bounds__(256)
   const int parts = s_parts;
   const int v = (threadIdx.x % LANES) * 4;
   for (int row = blockIdx.y * 32 + threadIdx.x / LANES; row < blockIdx.y * 32 + 32;
-       row += 256 / LANES) {
+       row += blockDim.x / LANES) {
     const int g = row / TA_ROWS, r = row % TA_ROWS;
     const int node = g * a.npt + r / a.group;
     if ((g > 0 && !h1.y) || r >= a.npt * a.group || node >= h0.w) continue;
@@ -913,7 +1029,7 @@ int ivc_tree_attention(const ivc_cache* c, int layer, const void* q, long long q
   for (int kv = 0; kv < 2; ++kv) {
     const unsigned long long d[2] = {static_cast<unsigned long long>(D), rows};
     const unsigned long long st[1] = {static_cast<unsigned long long>(D) * 2};
-    const unsigned box[2] = {64, static_cast<unsigned>(c->page_tokens)};
+    const unsigned box[2] = {64, static_cast<unsigned>(c->page_tokens < TA_KEYS ? c->page_tokens : TA_KEYS)};
     const bf16* base = static_cast<const bf16*>(kv ? c->v : c->k) + rows * D * layer;
     if (map_bf16(kv ? &vm : &km, 2, base, d, st, box) != IVC_OK) return IVC_ECUDA;
   }
