@@ -38,12 +38,12 @@
 // tokens by 0 in shared memory (0 x inf would reach every row); rows that do see
 // such a token get the non-finite value back in the epilogue.
 //
-// Warp 8 loads, warps 9 and 10 issue the MMAs of one group each, warp 11 mends value
-// tiles, warps 0-3 and 4-7 are the softmax groups. Two issuing warps, because an
-// MMA's issue takes as long as the MMA and a barrier wait 150 to 350 cycles even
-// when it is over: with one warp the waits of each 64-key step (about 1000 cycles)
-// added to its MMAs (760), now they pass behind the other group's MMAs. Every wait
-// is bounded (IVC_DEV_WAIT_TIMEOUT).
+// Warps 0-3 and 4-7 are the softmax groups, warp 8 loads queries and keys, warp 11
+// values, warps 9 and 10 issue the MMAs of one group each (and mend value tiles).
+// Two of each kind, because an MMA's issue takes as long as the MMA, a barrier wait
+// 150 to 350 cycles even when it is over and a load about 500: one warp's steps
+// would add up to more than the 1400 cycles in which HBM delivers a tile of 32 KB
+// to each SM. Every wait is bounded (IVC_DEV_WAIT_TIMEOUT).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -77,8 +77,14 @@ struct TreeArgs {
   int* start;                                // [grid] sequence in which a CTA's piece begins
   int4* head;                                // [2 grid] an item begun and not ended by a CTA
   float2* part_ml;                           // [2 grid][256] maximum (log2 units) and sum
-  float* part_o;                             // [2 grid][256][D]
+  float4* part_o;                            // [2 grid][D / 4][256] sums, 4 values of a row
 };
+
+// The tiles are cut into as many pieces as there are CTAs, or tiles if those are
+// fewer: piece i is tiles [total i / pieces, total (i + 1) / pieces), never empty.
+__device__ __forceinline__ int pieces_of(long long total, int grid) {
+  return total < grid ? static_cast<int>(total) : grid;
+}
 
 __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
 
@@ -140,15 +146,17 @@ __global__ void __launch_bounds__(1024)
   }
   __syncthreads();
   const long long total = s_prefix[a.B];
+  const int pieces = pieces_of(total, grid);
   for (int i = tid; i < grid; i += 1024) {
-    const long long pos = total * i / grid;  // the last sequence that begins at or before it
+    a.head[2 * i] = make_int4(0, 0, 0, 0);
+    if (i >= pieces) continue;
+    const long long pos = total * i / pieces;  // the last sequence that begins at or before it
     int lo = 0, hi = a.B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (s_prefix[mid] <= pos) lo = mid; else hi = mid;
     }
     a.start[i] = lo;
-    a.head[2 * i] = make_int4(0, 0, 0, 0);
   }
 }
 
@@ -170,9 +178,12 @@ struct Walk {
   int b;
   __device__ Walk(const TreeArgs& a) {
     const long long total = a.prefix[a.B];
-    pos = total * blockIdx.x / gridDim.x;
-    end = total * (blockIdx.x + 1) / gridDim.x;
-    b = a.start[blockIdx.x];
+    const int pieces = pieces_of(total, gridDim.x), i = blockIdx.x;
+    pos = end = 0;
+    if (i >= pieces) return;
+    pos = total * i / pieces;
+    end = total * (i + 1) / pieces;
+    b = a.start[i];
   }
   __device__ bool next(const ivc_cache& c, const TreeArgs& a, Item& it) {
     if (pos >= end) return false;
@@ -265,9 +276,9 @@ template <int D>
 struct TaSmem {
   static constexpr int HALVES = D / 64;
   static constexpr uint32_t SLOT = HALVES * TA_HALF;    // one tile of keys or values
-  static constexpr int SLOTS = 163840 / SLOT;           // 160 KB
+  static constexpr int SLOTS = 81920 / SLOT;            // of keys, and of values: 80 KB each
   static constexpr uint32_t Q = 2 * HALVES * TA_QHALF;  // two groups' rows
-  static constexpr uint32_t TOTAL = 1024 + Q + SLOTS * SLOT;
+  static constexpr uint32_t TOTAL = 1024 + Q + 2 * SLOTS * SLOT;
 };
 
 // The keys that a node sees in the tile at t0 as bits: committed tokens, and
@@ -294,6 +305,43 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// Value rows of the tile at `base` behind the committed tokens: those of drafted
+// tokens lose their non-finite values (and *odd tells so), those behind the
+// sequence become 0 up to the end of its last page (further ones were loaded as 0).
+// By one warp, in 16-byte pieces; the swizzle only permutes pieces within a row.
+template <int D>
+__device__ void mend_values(uint8_t* v, int base, int len, int n, int page_tokens, int* odd, int lane) {
+  const int drafted = max(0, len - base), behind = min(TA_KEYS, len + n - base);
+  const int end = min(TA_KEYS, div_up(len + n, page_tokens) * page_tokens - base);
+  bool found = false;
+  for (int i = lane; i < (end - drafted) * 8; i += 32) {
+    const int r = drafted + (i >> 3);
+#pragma unroll
+    for (int hf = 0; hf < D / 64; ++hf) {
+      uint4* at = reinterpret_cast<uint4*>(v + hf * TA_HALF + r * 128 + (i & 7) * 16);
+      if (r >= behind) {
+        *at = make_uint4(0u, 0u, 0u, 0u);
+        continue;
+      }
+      uint4 x = *at;
+      uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+      bool here = false;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if ((w[j] & 0x7f80u) == 0x7f80u) { w[j] &= 0xffff0000u; here = true; }
+        if ((w[j] & 0x7f800000u) == 0x7f800000u) { w[j] &= 0x0000ffffu; here = true; }
+      }
+      if (here) {
+        *at = x;
+        found = true;
+      }
+    }
+  }
+  if (found) *odd = 1;
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+}
+
 template <int D>
 __global__ void __launch_bounds__(TA_THREADS, 1)
     tree_attend_kernel(const __grid_constant__ CUtensorMap qmap,
@@ -305,35 +353,38 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
   uint8_t* sm = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sq = sm;
-  uint8_t* ring = sm + S::Q;
-  __shared__ __align__(8) uint64_t full[S::SLOTS], empty[S::SLOTS];
+  uint8_t* kring = sm + S::Q;
+  uint8_t* vring = kring + S::SLOTS * S::SLOT;
+  __shared__ __align__(8) uint64_t kfull[S::SLOTS], kempty[S::SLOTS];
+  __shared__ __align__(8) uint64_t vfull[S::SLOTS], vempty[S::SLOTS];
+  __shared__ __align__(8) uint64_t qfull[2], qempty[2];  // of each 128-row buffer
   __shared__ __align__(8) uint64_t sfull[2][2], pready[2][2], odone[2];  // [group][S buffer]
-  __shared__ __align__(8) uint64_t qfull, qempty, ofull, ofree, mlready;
-  __shared__ __align__(8) uint64_t mend[2], mended[2];
+  __shared__ __align__(8) uint64_t ofull, ofree, mlready, mended, seen;
   __shared__ uint32_t s_tmem;
-  __shared__ int s_mend_slot[2], s_odd[2];  // s_odd: a drafted value is not finite
-  __shared__ float2 s_ml[TA_ROWS];                    // group 1's maximum and sum
+  __shared__ int s_odd[2][2];       // [item & 1][issuer]: a drafted value is not finite
+  __shared__ float2 s_ml[TA_ROWS];  // group 1's maximum and sum
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::SLOTS; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 2);  // both issuers
+      mbar_init(&kfull[s], 1);
+      mbar_init(&kempty[s], 2);  // both issuers
+      mbar_init(&vfull[s], 1);
+      mbar_init(&vempty[s], 2);
     }
-    mbar_init(&qfull, 1);
-    mbar_init(&qempty, 2);
     for (int g = 0; g < 2; ++g) {
       for (int buf = 0; buf < 2; ++buf) {
         mbar_init(&sfull[g][buf], 1);
         mbar_init(&pready[g][buf], 4);
       }
       mbar_init(&odone[g], 1);
-      mbar_init(&mend[g], 1);
-      mbar_init(&mended[g], 1);
+      mbar_init(&qfull[g], 1);
+      mbar_init(&qempty[g], 2);
     }
     mbar_init(&ofull, 2);
     mbar_init(&ofree, 8);
     mbar_init(&mlready, 4);
-    s_odd[0] = s_odd[1] = 0;
+    mbar_init(&mended, 1);
+    mbar_init(&seen, 1);
     fence_mbar_init();
     tma_prefetch_desc(&qmap);
     tma_prefetch_desc(&kmap);
@@ -353,19 +404,21 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
   pdl_wait();     // the plan; everything before it in the stream
   pdl_trigger();  // the merge may launch; it waits for this grid
 
-  if (warp == 8) {
-    // ------------------------------------------------------------- producer
+  if (warp == 8 || warp == 11) {
+    // ------------------------------------------------------------- producers
+    const bool keys = warp == 8;
+    const CUtensorMap* map = keys ? &kmap : &vmap;
+    uint8_t* ring = keys ? kring : vring;
+    uint64_t* full = keys ? kfull : vfull;
+    uint64_t* empty = keys ? kempty : vempty;
     const int pt = c.page_tokens, box = min(pt, TA_KEYS), per_tile = TA_KEYS / box;
     const int pt_log = 31 - __clz(pt), box_log = 31 - __clz(box);
     const int nowhere = c.pages * c.kv_heads * pt;  // behind the last row: reads as 0
     Walk walk(a);
     Item it = {};
-    int slot = 0, round = 0, queries = 0, items = 0;
-    // Rows of the boxes (a page or half of one) of an item: lane l holds those of
-    // boxes base + l and base + 32 + l, so that the table is read 32 boxes ahead.
-    struct Rows {
-      int base, now, next;
-    };
+    int slot = 0, round = 0, queries = 0;
+    // rows of the boxes (a page or half of one) of an item: lane l holds those of
+    // boxes base + l and base + 32 + l, so that the table is read 32 boxes ahead
     auto row_of = [&](int b) -> int {
       const int token = b << box_log;
       if (token >= it.len + it.n) return nowhere;
@@ -376,71 +429,60 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
       }
       return (page * c.kv_heads + it.h) * pt + (token & (pt - 1));
     };
-    auto begin = [&](Rows& r) {
-      r.base = it.t0 * per_tile & ~31;
-      r.now = row_of(r.base + lane);
-      r.next = row_of(r.base + 32 + lane);
-    };
-    // one tile of keys or values
-    auto load = [&](const CUtensorMap* map, Rows& r, int tile) {
-      const int first = tile * per_tile;
-      if (first >= r.base + 32) {
-        r.base += 32;
-        r.now = r.next;
-        r.next = row_of(r.base + 32 + lane);
-      }
-      if (!warp_wait(&empty[slot], (round & 1) ^ 1)) return false;
-      uint8_t* dst = ring + slot * S::SLOT;
-      if (elect_one()) mbar_arrive_expect_tx(&full[slot], S::SLOT);
-      for (int i = 0; i < per_tile; ++i) {
-        const int row = __shfl_sync(0xffffffffu, r.now, (first + i) & 31);
-        if (elect_one()) {
-#pragma unroll
-          for (int hf = 0; hf < S::HALVES; ++hf)
-            tma_load_2d(dst + hf * TA_HALF + i * box * 128, map, &full[slot], 64 * hf, row);
-        }
-      }
-      __syncwarp();
-      if (++slot == S::SLOTS) {
-        slot = 0;
-        ++round;
-      }
-      return true;
-    };
-    auto load_q = [&]() {
-      if (!warp_wait(&qempty, (items & 1) ^ 1)) return false;
-      if (lane == 0) {
-        const int tiles = it.rows2 ? 2 : 1;
-        mbar_arrive_expect_tx(&qfull, tiles * S::HALVES * a.npt * a.group * 128);
-        for (int g = 0; g < tiles; ++g)
-          for (int hf = 0; hf < S::HALVES; ++hf)
-            tma_load_3d(sq + (g * S::HALVES + hf) * TA_QHALF, &qmap, &qfull, 64 * hf,
-                        it.h * a.group, it.row + it.node0 + g * a.npt);
-      }
+    // a 128-row buffer of queries, in turn
+    auto load_q = [&](int node0) {
+      const int buf = queries & 1;
+      if (!warp_wait(&qempty[buf], ((queries >> 1) & 1) ^ 1)) return false;
       ++queries;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&qfull[buf], S::HALVES * a.npt * a.group * 128);
+#pragma unroll
+        for (int hf = 0; hf < S::HALVES; ++hf)
+          tma_load_3d(sq + (buf * S::HALVES + hf) * TA_QHALF, &qmap, &qfull[buf], 64 * hf,
+                      it.h * a.group, node0);
+      }
       __syncwarp();
       return true;
     };
     while (ok && walk.next(c, a, it)) {
-      // in the order in which the MMAs first use them (see there); the queries,
-      // whose buffer the item before holds longest, after the first keys
-      const int ahead = it.rows2 ? 2 : 4, T = it.t1 - it.t0;
-      Rows krows, vrows;
-      begin(krows);
-      vrows = krows;
-      for (int t = 0; t < ahead && t < T && ok; ++t) ok = load(&kmap, krows, it.t0 + t);
-      if (ok) ok = load_q();
-      for (int t = 0; t < T && ok; ++t) {
-        ok = load(&vmap, vrows, it.t0 + t);
-        if (ok && t + ahead < T) ok = load(&kmap, krows, it.t0 + t + ahead);
+      if (keys) ok = load_q(it.row + it.node0);
+      if (ok && keys && it.rows2) ok = load_q(it.row + it.node0 + a.npt);
+      int base = it.t0 * per_tile & ~31;
+      int now = row_of(base + lane), next = row_of(base + 32 + lane);
+      for (int tile = it.t0; tile < it.t1 && ok; ++tile) {
+        const int first = tile * per_tile;
+        if (first >= base + 32) {
+          base += 32;
+          now = next;
+          next = row_of(base + 32 + lane);
+        }
+        int row[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) row[i] = __shfl_sync(0xffffffffu, now, (first + i) & 31);
+        ok = warp_wait(&empty[slot], (round & 1) ^ 1);
+        if (!ok) break;
+        if (elect_one()) {
+          uint8_t* dst = ring + slot * S::SLOT;
+          mbar_arrive_expect_tx(&full[slot], S::SLOT);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < per_tile)
+#pragma unroll
+              for (int hf = 0; hf < S::HALVES; ++hf)
+                tma_load_2d(dst + hf * TA_HALF + i * box * 128, map, &full[slot], 64 * hf, row[i]);
+        }
+        __syncwarp();
+        if (++slot == S::SLOTS) {
+          slot = 0;
+          ++round;
+        }
       }
-      ++items;
     }
     if (!ok) {  // let the copies in flight land
       const int loads = round * S::SLOTS + slot;
       for (int i = max(0, loads - S::SLOTS); i < loads; ++i)
         mbar_wait(&full[i % S::SLOTS], (i / S::SLOTS) & 1);
-      if (queries > 0) mbar_wait(&qfull, (queries - 1) & 1);
+      for (int i = max(0, queries - 2); i < queries; ++i) mbar_wait(&qfull[i & 1], (i >> 1) & 1);
     }
   } else if (warp == 9 || warp == 10) {
     // ------------------------------------------------------------- MMA issuers
@@ -452,33 +494,37 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
     const int g = warp - 9;
     const uint32_t idesc_s = idesc_bf16_f32(128, TA_KEYS);
     const uint32_t idesc_o = idesc_bf16_f32(128, D) | (1u << 16);  // B MN-major
-    const uint64_t kdesc = sw128_kmajor_desc(smem_u32(ring));
-    const uint64_t vdesc = sw128_mnmajor_desc(smem_u32(ring), TA_HALF);
+    const uint64_t kdesc = sw128_kmajor_desc(smem_u32(kring));
+    const uint64_t vdesc = sw128_mnmajor_desc(smem_u32(vring), TA_HALF);
     Walk walk(a);
     Item it = {};
-    int items = 0, mends = 0;
-    int slot = 0, round = 0;               // of the next load in order
-    uint32_t np = 0;                       // bit buffer: phase of the weights
+    int items = 0, mends = 0, queries = 0;
+    int ks = 0, kround = 0, vs = 0, vround = 0;  // the next tile's slots
+    uint32_t np = 0;                             // bit buffer: phase of the weights
+    auto advance = [&](int& slot, int& round) {
+      if (++slot == S::SLOTS) {
+        slot = 0;
+        ++round;
+      }
+    };
     while (ok && walk.next(c, a, it)) {
       const int U = it.units(), mine = (U + 1 - g) / 2;
       const bool all = it.rows2;           // every tile is used by both groups
-      const uint64_t qdesc = sw128_kmajor_desc(smem_u32(sq) + (all ? g : 0) * S::HALVES * TA_QHALF);
       const int T = it.t1 - it.t0, ahead = all ? 2 : 4;
-      struct Load {                        // a load in order: its slot and phase
-        int slot;
-        uint32_t parity;
-      };
-      auto next_load = [&]() {
-        const Load x{slot, static_cast<uint32_t>(round & 1)};
-        if (++slot == S::SLOTS) {
-          slot = 0;
-          ++round;
-        }
-        return x;
-      };
       auto own = [&](int t) { return all || (t & 1) == g; };
+      // the queries: one buffer, or group 0's and group 1's
+      const int qb = queries & 1, my_q = all ? qb ^ g : qb;
+      ok = warp_wait(&qfull[qb], (queries >> 1) & 1);
+      ++queries;
+      if (ok && all) {
+        ok = warp_wait(&qfull[queries & 1], (queries >> 1) & 1);
+        ++queries;
+      }
+      if (!ok) break;
+      const uint64_t qdesc = sw128_kmajor_desc(smem_u32(sq) + my_q * S::HALVES * TA_QHALF);
+      if (all && lane == 0) mbar_arrive(&qempty[my_q ^ 1]);  // the other group's buffer
       // by one lane: this group's scores with the keys of its unit i ...
-      auto issue_scores = [&](int ks, int i) {
+      auto issue_scores = [&](int i) {
         const uint64_t bd = kdesc + (ks * S::SLOT >> 4);
         const int buf = i & 1;
 #pragma unroll
@@ -488,11 +534,11 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
             umma_bf16(tmem + 128 * g + 64 * buf, qdesc + (hf * TA_QHALF >> 4) + 2 * kk,
                       bd + (hf * TA_HALF >> 4) + 2 * kk, idesc_s, (hf | kk) != 0);
         umma_commit(&sfull[g][buf]);
-        umma_commit(&empty[ks]);
-        if (i == mine - 1) umma_commit(&qempty);
+        umma_commit(&kempty[ks]);
+        if (i == mine - 1) umma_commit(&qempty[my_q]);
       };
       // ... and its weighted sum of the values of unit i
-      auto issue_sum = [&](int vs, int i) {
+      auto issue_sum = [&](int i) {
         const uint64_t bd = vdesc + (vs * S::SLOT >> 4);
         const int buf = i & 1;
 #pragma unroll
@@ -500,25 +546,25 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
           umma_bf16_ta(tmem + 256 + 128 * g, tmem + 128 * g + 64 * buf + 8 * kk,
                        bd + ((2048 * kk) >> 4), idesc_o, (i != 0 || kk != 0) ? 1u : 0u);
         umma_commit(&odone[g]);
-        umma_commit(&empty[vs]);
+        umma_commit(&vempty[vs]);
         if (i == mine - 1) umma_commit(&ofull);
       };
       for (int t = 0; t < ahead && t < T && ok; ++t) {
-        const Load k = next_load();
-        ok = warp_wait(&full[k.slot], k.parity);
-        if (ok && t == 0) ok = warp_wait(&qfull, items & 1);
+        ok = warp_wait(&kfull[ks], kround & 1);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          if (own(t)) issue_scores(k.slot, all ? t : t >> 1);
-          else mbar_arrive(&empty[k.slot]);
+          if (own(t)) issue_scores(all ? t : t >> 1);
+          else mbar_arrive(&kempty[ks]);
         }
         __syncwarp();
+        advance(ks, kround);
       }
       if (ok && mine == 0) {               // a single tile: nothing for group 1, which
         ok = warp_wait(&ofree, (items & 1) ^ 1);  // must not count for the item before
         if (ok && lane == 0) {
-          mbar_arrive(&qempty);
+          s_odd[items & 1][g] = 0;
+          mbar_arrive(&qempty[my_q]);
           mbar_arrive(&ofull);
         }
         __syncwarp();
@@ -526,40 +572,48 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
       int done = 0;                        // own units summed
       for (int t = 0; t < T && ok; ++t) {
         const bool more = t + ahead < T, mine_now = own(t);
-        const Load v = next_load();
-        Load k{0, 0};
-        if (more) k = next_load();
-        const int buf = done & 1, later = all ? t + ahead : (t + ahead) >> 1;
-        const bool mend_it = mine_now && (it.t0 + t + 1) * TA_KEYS > it.len;  // reaches behind
-        if (mend_it) {                                                        // the committed
-          if (!warp_wait(&full[v.slot], v.parity)) { ok = false; break; }
-          if (lane == 0 && (!all || g == 0)) {
-            s_mend_slot[g] = v.slot;
-            mbar_arrive(&mend[g]);
-          }
-        }
+        const int buf = done & 1;
         // the values, the weights and the keys of the scores that follow: one wait
         // for all three, and one branch with all MMAs of the step
         long long since = 0;
         while (!__all_sync(0xffffffffu,
-                           mbar_test(&full[v.slot], v.parity) &&
-                               (!more || mbar_test(&full[k.slot], k.parity)) &&
+                           mbar_test(&vfull[vs], vround & 1) &&
+                               (!more || mbar_test(&kfull[ks], kround & 1)) &&
                                (!mine_now || mbar_test(&pready[g][buf], (np >> buf) & 1)))) {
           const long long now = clock64();
           if (since == 0) since = now;
           if (__any_sync(0xffffffffu, now - since > IVC_WAIT_CYCLES)) { ok = false; break; }
         }
-        if (ok && mend_it) ok = warp_wait(&mended[g], mends++ & 1);
-        if (ok && mine_now && done == 0) ok = warp_wait(&ofree, (items & 1) ^ 1);
+        if (ok && mine_now && done == 0) {
+          ok = warp_wait(&ofree, (items & 1) ^ 1);
+          if (lane == 0) s_odd[items & 1][g] = 0;  // no epilogue reads it any more
+        }
         if (!ok) break;
+        const int tile = it.t0 + t;
+        if (mine_now && (tile + 1) * TA_KEYS > it.len) {  // reaches behind the committed tokens
+          if (!all || g == 0) {
+            __syncwarp();
+            mend_values<D>(vring + vs * S::SLOT, tile * TA_KEYS, it.len, it.n, c.page_tokens,
+                           &s_odd[items & 1][g], lane);
+          }
+          if (all && g == 0) {  // the other issuer, which has seen the tile before
+            ok = warp_wait(&seen, (mends & 1) ^ 1);
+            if (ok && lane == 0) mbar_arrive(&mended);
+            ++mends;
+          } else if (all) {
+            ok = warp_wait(&mended, mends++ & 1);
+            if (ok && lane == 0) mbar_arrive(&seen);
+          }
+          if (!ok) break;
+        }
         tc_fence_after();
         if (elect_one()) {
           if (mine_now) {
-            issue_sum(v.slot, done);
-            if (more) issue_scores(k.slot, later);
+            issue_sum(done);
+            if (more) issue_scores(all ? t + ahead : (t + ahead) >> 1);
           } else {
-            mbar_arrive(&empty[v.slot]);
-            if (more) mbar_arrive(&empty[k.slot]);
+            mbar_arrive(&vempty[vs]);
+            if (more) mbar_arrive(&kempty[ks]);
           }
         }
         __syncwarp();
@@ -567,60 +621,8 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
           np ^= 1u << buf;
           ++done;
         }
-      }
-      ++items;
-    }
-  } else if (warp == 11) {
-    // ------------------------------------------------- value tiles at the end
-    Walk walk(a);
-    Item it = {};
-    int mends[2] = {0, 0}, items = 0;
-    while (ok && walk.next(c, a, it)) {
-      const int first = max(it.t0, it.len / TA_KEYS);
-      for (int tile = first; tile < it.t1 && ok; ++tile) {
-        const int g = it.rows2 ? 0 : (tile - it.t0) & 1;  // the issuer that asks
-        ok = warp_wait(&mend[g], mends[g]++ & 1);
-        if (!ok) break;
-        // (no epilogue reads the flag of two items before any more)
-        if (tile == first && lane == 0) s_odd[items & 1] = 0;
-        __syncwarp();
-        uint8_t* v = ring + s_mend_slot[g] * S::SLOT;
-        const int base = tile * TA_KEYS;
-        const int drafted = max(0, it.len - base);                    // first drafted row
-        const int behind = min(TA_KEYS, it.len + it.n - base);       // first row behind them
-        const int pages_end = min(TA_KEYS, div_up(it.len + it.n, c.page_tokens) * c.page_tokens - base);
-        bool odd = false;
-        // 16-byte pieces; the swizzle only permutes pieces within a row
-        for (int i = lane; i < (pages_end - drafted) * 8; i += 32) {
-          const int r = drafted + (i >> 3);
-#pragma unroll
-          for (int hf = 0; hf < S::HALVES; ++hf) {
-            uint4* at = reinterpret_cast<uint4*>(v + hf * TA_HALF + r * 128 + (i & 7) * 16);
-            if (r >= behind) {
-              *at = make_uint4(0u, 0u, 0u, 0u);
-              continue;
-            }
-            uint4 x = *at;
-            uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-            bool here = false;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if ((w[j] & 0x7f80u) == 0x7f80u) { w[j] &= 0xffff0000u; here = true; }
-              if ((w[j] & 0x7f800000u) == 0x7f800000u) { w[j] &= 0x0000ffffu; here = true; }
-            }
-            if (here) {
-              *at = x;
-              odd = true;
-            }
-          }
-        }
-        if (odd) s_odd[items & 1] = 1;
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&mended[g]);
-          if (it.rows2) mbar_arrive(&mended[1]);
-        }
+        advance(vs, vround);
+        if (more) advance(ks, kround);
       }
       ++items;
     }
@@ -780,8 +782,8 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
         const int prow = (it.rows2 ? g * TA_ROWS : 0) + r;
         bf16* dst = a.out + (static_cast<long long>(it.row + node) * a.q_heads +
                              it.h * a.group + r % a.group) * D;
-        float* part = a.part_o + (static_cast<size_t>(slot) * 256 + prow) * D;
-        const bool odd = it.t1 * TA_KEYS > it.len && s_odd[items & 1] != 0;
+        float4* part = a.part_o + static_cast<size_t>(slot) * (D / 4) * 256 + prow;
+        const bool odd = it.t1 * TA_KEYS > it.len && (s_odd[items & 1][0] | s_odd[items & 1][1]) != 0;
 #pragma unroll 1
         for (int d = 0; d < D; d += 32) {
           __syncwarp();
@@ -829,10 +831,11 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
               to16[j] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           } else {
-            uint4* to16 = reinterpret_cast<uint4*>(part + d);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              to16[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            for (int j = 0; j < 8; ++j)  // neighbouring lanes, neighbouring 16 bytes
+              part[(d / 4 + j) * 256] =
+                  make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
+                              __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
           }
         }
         if (write && !whole)
@@ -862,65 +865,65 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
 // ------------------------------------------------------------------ merge
 // Block (i, y): rows 32 y .. 32 y + 31 of the item that CTA i began and did not
 // end. Its parts are CTA i's and, in order, the first ones of the CTAs after it.
+// Lane = row, warp = 16 of its values.
 template <int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(2 * D)
     tree_merge_kernel(const __grid_constant__ ivc_cache c, const __grid_constant__ TreeArgs a,
                       int grid) {
   pdl_wait();
   pdl_trigger();
   const int i = blockIdx.x;
-  const int4 h0 = a.head[2 * i], h1 = a.head[2 * i + 1];
+  const int4 h0 = a.head[2 * i];  // {1, first row of the sequence, first node, nodes}
   if (h0.x != 1) return;
-  constexpr int LANES = D / 4;  // a row's lanes, 4 values each
-  __shared__ int s_slot[TA_MAX_GRID];
-  __shared__ int s_parts;
-  if (threadIdx.x == 0) {
-    s_slot[0] = 2 * i + 1;
-    s_parts = 1;
-  }
-  __syncthreads();
-  {
-    const long long total = a.prefix[a.B];
-    const long long item_end = total * (i + 1) / grid + h1.z;
-    for (int j = i + 1 + threadIdx.x; j < grid; j += blockDim.x) {
-      const long long pos = total * j / grid;
-      if (pos >= item_end) break;
-      s_slot[j - i] = pos < total * (j + 1) / grid ? 2 * j : -1;  // -1: an empty piece
-      atomicMax(&s_parts, j - i + 1);
+  const int4 h1 = a.head[2 * i + 1];  // {kv head, more than 128 rows, tiles that follow, 0}
+  const int row = blockIdx.y * 32 + (threadIdx.x & 31), warp = threadIdx.x >> 5;
+  const int g = row / TA_ROWS, r = row % TA_ROWS;
+  const int node = g * a.npt + r / a.group;
+  const bool live = (g == 0 || h1.y) && r < a.npt * a.group && node < h0.w;
+  if (!__any_sync(0xffffffffu, live)) return;
+  // its parts: the pieces that begin before it ends
+  const long long total = a.prefix[a.B];
+  const int pieces = pieces_of(total, grid);
+  const long long item_end = total * (i + 1) / pieces + h1.z;
+  const int parts =
+      static_cast<int>(min(static_cast<long long>(pieces), (item_end * pieces + total - 1) / total)) - i;
+  auto slot = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * i + 1 : 2 * (i + k)); };
+  float m = -INFINITY;
+#pragma unroll 4
+  for (int k = 0; k < parts; ++k)
+    if (live) m = fmaxf(m, a.part_ml[slot(k) * 256 + row].x);
+  float l = 0.f;
+  float o[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) o[e] = 0.f;
+#pragma unroll 2
+  for (int k = 0; k < parts; ++k) {
+    if (!live) continue;
+    const float2 ml = a.part_ml[slot(k) * 256 + row];
+    const float4* from = a.part_o + (slot(k) * (D / 4) + 4 * warp) * 256 + row;
+    const float4 x[4] = {from[0], from[256], from[512], from[768]};
+    if (ml.x == -INFINITY && ml.y == 0.f) continue;  // it saw nothing in that part
+    const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
+    l += ml.y * f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      o[4 * e] += x[e].x * f;
+      o[4 * e + 1] += x[e].y * f;
+      o[4 * e + 2] += x[e].z * f;
+      o[4 * e + 3] += x[e].w * f;
     }
   }
-  __syncthreads();
-  const int parts = s_parts;
-  const int v = (threadIdx.x % LANES) * 4;
-  for (int row = blockIdx.y * 32 + threadIdx.x / LANES; row < blockIdx.y * 32 + 32;
-       row += blockDim.x / LANES) {
-    const int g = row / TA_ROWS, r = row % TA_ROWS;
-    const int node = g * a.npt + r / a.group;
-    if ((g > 0 && !h1.y) || r >= a.npt * a.group || node >= h0.w) continue;
-    auto slot = [&](int k) { return static_cast<size_t>(s_slot[k]) * 256 + row; };
-    float m = -INFINITY;
-    for (int k = 0; k < parts; ++k)
-      if (s_slot[k] >= 0) m = fmaxf(m, a.part_ml[slot(k)].x);
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < parts; ++k) {
-      if (s_slot[k] < 0) continue;
-      const float2 ml = a.part_ml[slot(k)];
-      if (ml.x == -INFINITY && ml.y == 0.f) continue;  // it saw nothing in that part
-      const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - m);
-      const float4 x = *reinterpret_cast<const float4*>(a.part_o + slot(k) * D + v);
-      l += ml.y * f;
-      o.x += x.x * f;
-      o.y += x.y * f;
-      o.z += x.z * f;
-      o.w += x.w * f;
-    }
-    const float inv = 1.f / l;
-    bf16* dst = a.out + (static_cast<long long>(h0.y + h0.z + node) * a.q_heads + h1.x * a.group +
-                         r % a.group) * D + v;
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o.x * inv, o.y * inv),
-                                                pack_bf16(o.z * inv, o.w * inv));
-  }
+  if (!live) return;
+  const float inv = 1.f / l;
+  uint4* dst = reinterpret_cast<uint4*>(
+      a.out + (static_cast<long long>(h0.y + h0.z + node) * a.q_heads + h1.x * a.group +
+               r % a.group) * D + 16 * warp);
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    dst[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv),
+                        pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                        pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                        pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
 }
 
 int tree_grid() { return num_sms() < TA_MAX_GRID ? num_sms() : TA_MAX_GRID; }
@@ -947,7 +950,7 @@ size_t carve(TreeArgs* a, char* ws, int B, int grid, int D) {
     a->start = reinterpret_cast<int*>(start);
     a->head = reinterpret_cast<int4*>(head);
     a->part_ml = reinterpret_cast<float2*>(ml);
-    a->part_o = reinterpret_cast<float*>(o);
+    a->part_o = reinterpret_cast<float4*>(o);
   }
   return at;
 }
@@ -968,7 +971,7 @@ int run_tree(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm
       return rc;
   }
   TraceScope ts("tree.merge", s);
-  return launch_k(tree_merge_kernel<D>, dim3(grid, 8), dim3(256), 0, s, 1, c, a, grid);
+  return launch_k(tree_merge_kernel<D>, dim3(grid, 8), dim3(2 * D), 0, s, 1, c, a, grid);
 }
 
 }  // namespace
