@@ -355,38 +355,45 @@ __global__ void __launch_bounds__(CA_THREADS)
 }
 
 // Copies the jobs' rows in every layer, head, and of keys and values: one
-// (job, plane, head) is rows * head_dim contiguous values. Bound by HBM.
-__global__ void __launch_bounds__(256) cache_copy_kernel(ivc_cache c, ForkPlan plan) {
+// (job, plane, head) is rows * head_dim contiguous values, taken in chunks of 4 KB,
+// a warp each with all of its loads in flight. (A CTA per (job, plane, head) left
+// three quarters of its threads idle for 16-token pages.) Bound by HBM.
+constexpr int CC_PIECES = 8;  // 16-byte pieces per lane and chunk
+__global__ void __launch_bounds__(256, 4) cache_copy_kernel(ivc_cache c, ForkPlan plan) {
   pdl_wait();
   pdl_trigger();
-  const int per_row = c.head_dim / 8;  // 16-byte pieces
-  const long long heads = c.kv_heads;
-  const long long units = static_cast<long long>(*plan.n_jobs) * c.layers * 2 * heads;
-  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const int h = static_cast<int>(u % heads);
-    const long long rest = u / heads;
-    const int plane = static_cast<int>(rest % (2 * c.layers));
-    const int4 job = plan.jobs[rest / (2 * c.layers)];
-    if (!page_ok(c, job.x) || !page_ok(c, job.y)) continue;
+  const int lane = threadIdx.x & 31;
+  const unsigned per_row = c.head_dim / 8;  // 16-byte pieces
+  const unsigned heads = c.kv_heads, planes = 2 * c.layers;
+  const unsigned block = c.page_tokens * per_row;                       // a page of one head
+  const unsigned chunks = (block + 32 * CC_PIECES - 1) / (32 * CC_PIECES);
+  const unsigned long long units =
+      static_cast<unsigned long long>(*plan.n_jobs) * planes * heads * chunks;
+  const unsigned long long step = static_cast<unsigned long long>(gridDim.x) * (blockDim.x / 32);
+  for (unsigned long long u = static_cast<unsigned long long>(blockIdx.x) * (blockDim.x / 32) +
+                              (threadIdx.x >> 5);
+       u < units; u += step) {
+    // chunk fastest, then head, plane, job
+    const unsigned per_job = planes * heads * chunks;                  // < 2^32: see cache_ok
+    const unsigned job_no = static_cast<unsigned>(u / per_job);
+    unsigned rest = static_cast<unsigned>(u - static_cast<unsigned long long>(job_no) * per_job);
+    const unsigned chunk = rest % chunks;
+    rest /= chunks;
+    const unsigned h = rest % heads, plane = rest / heads;
+    const int4 job = plan.jobs[job_no];
+    const unsigned pieces = job.z * per_row, first = chunk * 32 * CC_PIECES + lane;
+    if (chunk * 32 * CC_PIECES >= pieces || !page_ok(c, job.x) || !page_ok(c, job.y)) continue;
     uint4* base = static_cast<uint4*>(plane & 1 ? c.v : c.k);
-    const size_t block = static_cast<size_t>(c.page_tokens) * per_row;
-    const size_t first = static_cast<size_t>(plane >> 1) * c.pages;
-    const uint4* from = base + ((first + job.x) * heads + h) * block;
-    uint4* to = base + ((first + job.y) * heads + h) * block;
-    const int pieces = job.z * per_row;
-    for (int i0 = 0; i0 < pieces; i0 += 4 * 256) {
-      uint4 r[4];
+    const size_t layer = static_cast<size_t>(plane >> 1) * c.pages;
+    const uint4* from = base + ((layer + job.x) * heads + h) * block;
+    uint4* to = base + ((layer + job.y) * heads + h) * block;
+    uint4 r[CC_PIECES];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = i0 + k * 256 + threadIdx.x;
-        if (i < pieces) r[k] = from[i];
-      }
+    for (int k = 0; k < CC_PIECES; ++k)
+      if (first + 32 * k < pieces) r[k] = from[first + 32 * k];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = i0 + k * 256 + threadIdx.x;
-        if (i < pieces) to[i] = r[k];
-      }
-    }
+    for (int k = 0; k < CC_PIECES; ++k)
+      if (first + 32 * k < pieces) to[first + 32 * k] = r[k];
   }
 }
 
@@ -478,54 +485,72 @@ __global__ void __launch_bounds__(CA_THREADS)
 // Moves the kept tokens of one sequence, plane (layer, keys or values) and
 // group of heads, in place. Targets do not lie behind their sources and rise
 // with them, so a chunk of rows that is read whole before any of it is written
-// cannot spoil a later chunk's sources. Bound by HBM.
-constexpr int MV_PIECES = 8;  // 16-byte pieces a thread holds
-__global__ void __launch_bounds__(256)
+// cannot spoil a later chunk's sources; the next chunk's loads are issued before
+// this one's stores (its sources lie behind these targets). Bound by HBM.
+constexpr int MV_THREADS = 256;
+constexpr int MV_PIECES = 4;  // 16-byte pieces a thread holds of a chunk
+__global__ void __launch_bounds__(MV_THREADS, 4)
     cache_move_kernel(ivc_cache c, CompactPlan plan, int stride, int head_groups,
                       int heads_per_group) {
   pdl_wait();
   pdl_trigger();
   const int i = blockIdx.x / head_groups;
-  const int h0 = (blockIdx.x % head_groups) * heads_per_group;
-  const int heads = min(heads_per_group, c.kv_heads - h0);
+  const unsigned h0 = (blockIdx.x % head_groups) * heads_per_group;
+  const unsigned heads = min(heads_per_group, c.kv_heads - static_cast<int>(h0));
   const int plane = blockIdx.y;
   const int n = plan.count[i];
-  const int per_row = c.head_dim / 8;
-  const int pt = c.page_tokens;
+  if (n == 0) return;
+  const int row_log = c.head_dim == 64 ? 3 : 4;          // 16-byte pieces of a row
+  const int pt_log = 31 - __clz(c.page_tokens);
   const int2* rows = plan.rows + static_cast<size_t>(i) * stride;
   uint4* base = static_cast<uint4*>(plane & 1 ? c.v : c.k) +
-                static_cast<size_t>(plane >> 1) * c.pages * c.kv_heads * pt * per_row;
-  // piece x of the group: 16 bytes of head x / per_row % heads of kept token
-  // x / (per_row * heads)
-  const unsigned pieces = static_cast<unsigned>(n) * heads * per_row;  // < 2^31: see below
-  auto at = [&](int slot, int h, int piece) {
-    const size_t page = slot / pt;
-    return ((page * c.kv_heads + h0 + h) * pt + slot % pt) * per_row + piece;
+                ((static_cast<size_t>(plane >> 1) * c.pages * c.kv_heads) << (pt_log + row_log));
+  // piece x of the group: 16 bytes of head x / 2^row_log % heads of kept token
+  // x / 2^row_log / heads
+  const unsigned pieces = (static_cast<unsigned>(n) * heads) << row_log;  // < 2^31: see below
+  auto at = [&](int slot, unsigned h, unsigned piece) {
+    const size_t page = slot >> pt_log;
+    return ((((page * c.kv_heads + h0 + h) << pt_log) + (slot & (c.page_tokens - 1))) << row_log) + piece;
   };
-  for (unsigned x0 = 0; x0 < pieces; x0 += MV_PIECES * 256) {
+  struct Chunk {
     uint4 r[MV_PIECES];
-    size_t to[MV_PIECES];
-    bool moved[MV_PIECES];
+    int slot[MV_PIECES];  // the target, -1: nothing to move
+  };
+  auto split = [&](unsigned x, unsigned& h, unsigned& piece) {
+    piece = x & ((1u << row_log) - 1);
+    const unsigned token = (x >> row_log) / heads;
+    h = (x >> row_log) - token * heads;
+    return token;
+  };
+  auto load = [&](Chunk& k, unsigned x0) {
 #pragma unroll
-    for (int k = 0; k < MV_PIECES; ++k) {
-      const unsigned x = x0 + k * 256 + threadIdx.x;
-      moved[k] = false;
+    for (int e = 0; e < MV_PIECES; ++e) {
+      const unsigned x = x0 + e * MV_THREADS + threadIdx.x;
+      k.slot[e] = -1;
       if (x < pieces) {
-        const int piece = static_cast<int>(x % per_row);
-        const int h = static_cast<int>(x / per_row % heads);
-        const int2 row = rows[x / per_row / heads];
+        unsigned h, piece;
+        const int2 row = rows[split(x, h, piece)];
         if (row.x != row.y) {
-          moved[k] = true;
-          r[k] = base[at(row.x, h, piece)];
-          to[k] = at(row.y, h, piece);
+          k.slot[e] = row.y;
+          k.r[e] = base[at(row.x, h, piece)];
         }
       }
     }
-    __syncthreads();
+  };
+  Chunk now, next;
+  load(now, 0);
+  for (unsigned x0 = 0; x0 < pieces; x0 += MV_PIECES * MV_THREADS) {
+    const bool more = x0 + MV_PIECES * MV_THREADS < pieces;
+    if (more) load(next, x0 + MV_PIECES * MV_THREADS);
+    __syncthreads();  // the chunk is read
 #pragma unroll
-    for (int k = 0; k < MV_PIECES; ++k)
-      if (moved[k]) base[to[k]] = r[k];
-    __syncthreads();
+    for (int e = 0; e < MV_PIECES; ++e)
+      if (now.slot[e] >= 0) {
+        unsigned h, piece;
+        split(x0 + e * MV_THREADS + threadIdx.x, h, piece);
+        base[at(now.slot[e], h, piece)] = now.r[e];
+      }
+    if (more) now = next;
   }
 }
 
@@ -635,7 +660,7 @@ int ivc_cache_fork(const ivc_cache* c, const int32_t* src, const int32_t* dst, i
     if (rc != IVC_OK) return rc;
   }
   TraceScope ts("cache.copy", s);
-  return launch_k(cache_copy_kernel, dim3(8 * num_sms()), dim3(256), 0, s, 1, *c, plan);
+  return launch_k(cache_copy_kernel, dim3(4 * num_sms()), dim3(256), 0, s, 1, *c, plan);
 }
 
 int ivc_cache_compact(const ivc_cache* c, const int32_t* count, const int32_t* keep,
@@ -660,17 +685,17 @@ int ivc_cache_compact(const ivc_cache* c, const int32_t* count, const int32_t* k
     if (rc != IVC_OK) return rc;
   }
   if (stride == 0) return IVC_OK;
-  // one CTA's chunk is MV_PIECES * 256 pieces: few kept tokens share a CTA over
+  // two of a CTA's chunks are 2 * MV_PIECES * MV_THREADS pieces: few kept tokens share a CTA over
   // several heads, many get a CTA per head. (A sequence's tokens are at most
   // pages * page_tokens <= 2^27, 16 pieces each, and only strides of at most one
   // chunk share a CTA, so a CTA's pieces are counted in 32 bits.)
-  const int per_chunk = MV_PIECES * 256 / (c->head_dim / 8);
+  const int per_chunk = 2 * MV_PIECES * MV_THREADS / (c->head_dim / 8);
   int per_group = per_chunk / stride;
   per_group = per_group < 1 ? 1 : per_group > c->kv_heads ? c->kv_heads : per_group;
   const int groups = (c->kv_heads + per_group - 1) / per_group;
   TraceScope ts("cache.move", s);
   return launch_k(cache_move_kernel, dim3(static_cast<unsigned>(n) * groups, 2 * c->layers),
-                  dim3(256), 0, s, 1, *c, plan, stride, groups, per_group);
+                  dim3(MV_THREADS), 0, s, 1, *c, plan, stride, groups, per_group);
 }
 
 }  // extern "C"
