@@ -346,7 +346,9 @@ int ivc_assemble_sequence(const int32_t* input_ids, const int32_t* seq_offsets, 
  * shared it: such pages are full, and no call writes into them.
  *   page_tokens 16, 32, 64 or 128; head_dim 64 or 128; pages <= 2^20;
  *   max_seqs <= 65536; one layer's pages * kv_heads * page_tokens < 2^31.
- * All pointers are caller-owned device memory; k and v 16-byte aligned.
+ * All pointers are caller-owned device memory; k and v 16-byte aligned. Calls
+ * that change a cache, and calls that read what another one changes, are
+ * ordered by the caller (one stream, or events).
  * ivc_cache_init makes every sequence empty and every page free; it leaves k
  * and v as they are (rows that no token was written to are never used). */
 typedef struct ivc_cache {

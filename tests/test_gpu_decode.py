@@ -718,3 +718,140 @@ def test_calls_on_another_stream_and_without_workspaces():
         got = ivc.tree_attention(p.gpu, 0, q, None, off, stream=s)
     s.synchronize()
     assert torch.equal(got, want)
+
+
+def test_pages_beyond_32_bit_offsets():
+    """A cache of 5 GB a layer: the same step in its last pages of layer 1 and in a
+    small cache gives the same bits."""
+    ivc = _ivc()
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 22 GB of device memory")
+    Hq, kv, pt, D_ = 8, 8, 128, 128
+    par, off = dev([-1, 0, 0, 1, 1, 2, -1, 0, 1]), dev([0, 6, 9])
+
+    def step(pages, first):
+        c = ivc.Cache.empty(2, pages, kv, pt, D_, 3, 8)
+        order = torch.arange(first, first + 8, dtype=torch.int32, device="cuda")
+        c.free_list[-8:] = order            # taken from the last one down
+        ws = ivc.new_workspace(ivc.tree_attention_workspace_size(c, 9, Hq, 2))
+        pre = dev([300, 100])
+        g = torch.Generator(device="cuda").manual_seed(9)
+        outs = []
+        for counts, parents, offs in ((pre, None, dev([0, 300, 400])), (dev([6, 3]), par, off)):
+            n = int(offs[-1])
+            ivc.cache_reserve(c, counts, workspace=ws)
+            for layer in (0, 1):
+                x = torch.randn(n, (Hq + 2 * kv) * D_, generator=g, device="cuda").bfloat16()
+                one = torch.ones(D_, dtype=torch.bfloat16, device="cuda")
+                q = ivc.qk_norm_rope(c, layer, x, one, one, dev(range(n)), offs, workspace=ws)
+                if parents is not None:
+                    outs.append(ivc.tree_attention(c, layer, q, parents, offs, workspace=ws))
+            if parents is None:
+                ivc.cache_compact(c, counts)
+        ivc.cache_compact(c, dev([3, 1]), dev([[0, 2, 5], [1, 0, 0]]))
+        ivc.cache_fork(c, dev([0]), dev([2]), False)
+        for s, n in ((0, 303), (1, 101), (2, 303)):
+            pages_of = c.table[s, :-(-n // pt)].long()
+            for x in (c.k, c.v):
+                outs.append(x[1, pages_of].transpose(1, 2).reshape(-1, kv, D_)[:n])
+        assert ivc.device_status(ws) == 0
+        return outs
+
+    small = step(12, 4)
+    far = step(20000, 19992)
+    assert all(torch.equal(a, b) for a, b in zip(small, far))
+    assert torch.equal(far[2], far[6])
+
+
+def test_two_streams_with_their_own_workspaces_and_two_graphs():
+    """Attention over one cache from two streams at once, eager and as replayed
+    graphs, each with its own workspace."""
+    lens, counts = [900, 77, 300], [9, 1, 20]
+    ivc, p, q, trees, off = _attend_case(lens, counts, 16, 2, 32, 128, "tree")
+    par, off = dev(sum(trees, [])), dev(off)
+    want = ivc.tree_attention(p.gpu, 0, q, par, off), ivc.tree_attention(p.gpu, 1, q, par, off)
+    size = ivc.tree_attention_workspace_size(p.gpu, 30, 16, 3)
+    spaces = [ivc.new_workspace(size) for _ in range(2)]
+    outs = [torch.empty_like(want[0]) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    graphs = []
+    torch.cuda.synchronize()
+    for layer, (s, ws, o) in enumerate(zip(streams, spaces, outs)):
+        for _ in range(4):
+            ivc.tree_attention(p.gpu, layer, q, par, off, out=o, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    for layer, (ws, o) in enumerate(zip(spaces, outs)):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ivc.tree_attention(p.gpu, layer, q, par, off, out=o, workspace=ws)
+        graphs.append(g)
+        o.zero_()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert [ivc.device_status(ws) for ws in spaces] == [0, 0]
+
+
+@pytest.mark.parametrize("B,Hq,kv,D_,pt", [(300, 4, 2, 64, 16), (4096, 2, 1, 64, 32), (70, 24, 8, 128, 64)])
+def test_tree_attention_many_short_sequences(B, Hq, kv, D_, pt):
+    """More items than CTAs, empty sequences among them, against torch in float64."""
+    ivc = _ivc()
+    rng = np.random.RandomState(B)
+    lens, counts = rng.randint(0, 150, B), rng.randint(0, 4, B)
+    need = -(-(lens + counts) // pt)
+    c = ivc.Cache.empty(1, int(need.sum()) + 1, kv, pt, D_, B, int(need.max()) + 1)
+    c.k.normal_()
+    c.v.normal_()
+    ivc.cache_reserve(c, dev(lens))
+    ivc.cache_compact(c, dev(lens))
+    ivc.cache_reserve(c, dev(counts))
+    N = int(counts.sum())
+    q = torch.randn(N, Hq, D_, device="cuda").bfloat16()
+    off = dev(np.concatenate([[0], np.cumsum(counts)]))
+    ws = ivc.new_workspace(ivc.tree_attention_workspace_size(c, N, Hq, B))
+    got = ivc.tree_attention(c, 0, q, None, off, workspace=ws)
+    assert ivc.device_status(ws) == 0
+    row = 0
+    for b in range(B):
+        n, m = int(counts[b]), int(lens[b])
+        if n == 0:
+            continue
+        pages = c.table[b, :need[b]].long()
+        k, v = (x[0, pages].transpose(1, 2).reshape(-1, kv, D_)[:m + n].double()
+                .repeat_interleave(Hq // kv, 1) for x in (c.k, c.v))
+        s = torch.einsum("nhd,lhd->hnl", q[row:row + n].double(), k) * D_ ** -0.5
+        see = torch.ones(n, m + n, dtype=torch.bool, device="cuda").tril(m)
+        w = torch.softmax(s.masked_fill(~see, float("-inf")), -1)
+        want, size = torch.einsum("hnl,lhd->nhd", w, v), torch.einsum("hnl,lhd->nhd", w, v.abs())
+        err = (got[row:row + n].double() - want).abs()
+        assert bool((err <= BF * want.abs() + (BF + 2.0 ** -14) * size).all()), b
+        row += n
+
+
+def test_cache_many_sequences_in_one_call():
+    """More sequences than a CTA has threads: one reserve, fork, compact and free."""
+    ivc = _ivc()
+    n, pt = 1500, 16
+    p = Pair(ivc, layers=1, pages=4 * n, kv_heads=1, pt=pt, seqs=2 * n, max_pages=3)
+    p.ws = ivc.new_workspace(ivc.cache_workspace_size(p.gpu, n, 8))
+    rng = np.random.RandomState(0)
+    seqs = rng.permutation(2 * n)[:n].tolist()
+    rest = [s for s in range(2 * n) if s not in set(seqs)]
+    lens = rng.randint(0, 3 * pt, n).tolist()
+    p.reserve(lens, seqs)
+    p.compact(lens, seqs=seqs)
+    p.fork(seqs, rest, True)
+    # every third copy keeps up to eight tokens of what it alone holds
+    start = [x // pt * pt for x in lens]
+    keep = [sorted(rng.permutation(max(x - a, 1))[:8].tolist()) for x, a in zip(lens, start)]
+    count = [0 if x == a else min(len(k), 8) for x, a, k in zip(lens, start, keep)]
+    keep = [(k + [0] * 8)[:8] for k in keep]
+    p.compact(count, keep, start, rest)
+    p.free(rest[:n // 2] + seqs[n // 2:])
+    p.free(rest[n // 2:] + seqs[:n // 2])
+    assert len(p.ref.free) == 4 * n
