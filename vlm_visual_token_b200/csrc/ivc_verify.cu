@@ -14,9 +14,15 @@
 //
 // A sequence is one cluster of 8 CTAs: each walks for itself (the same scalars) and
 // sums a contiguous eighth of the vocabulary, and the eight sums are exchanged
-// through distributed shared memory. Bound by HBM for a batch (the rows of the
-// nodes with rejections are read once from HBM and again from L2), by the chain
-// of dependent loads (offsets, tokens, probabilities, row) for one sequence.
+// through distributed shared memory. One sequence without a rejection is bound by
+// its chain of dependent loads (offsets, tokens, probabilities, row): 7 us for 151001
+// tokens. A rejection with draft probabilities adds a pass of about 4 us, bound by
+// the fp64 and conversion pipes of the cluster's SMs;
+// a batch takes as long as its longest chain of them: 48 trees of 16 nodes 55 us,
+// without rejections 16 us (their rows in one read from HBM would be 9 us).
+// 384 threads of 80 registers: 512 threads spill, 256 take 8.1 us for one sequence.
+// Clusters of 16 halve a pass but fewer fit: 52 us for the trees, 19 us without
+// rejections.
 #include <cuda_runtime.h>
 
 #include "ivc_internal.h"
@@ -25,6 +31,8 @@
 namespace ivc {
 namespace {
 
+constexpr int VF_THREADS = 384;
+constexpr int VF_WARPS = VF_THREADS / 32;
 constexpr int VF_CLUSTER = 8;
 constexpr int VF_SMALL = 4096;  // a vocabulary up to this size is one CTA's
 constexpr int VF_BATCH = 8;     // values a thread has in flight
@@ -129,10 +137,9 @@ __device__ void exchange(Sums& sums, int pass, double mine) {
   cluster_sync();
 }
 
-template <int CL, int VF_THREADS, int PER_SM>
-__global__ void __launch_bounds__(VF_THREADS, PER_SM)
+template <int CL>
+__global__ void __launch_bounds__(VF_THREADS, 2)
     verify_kernel(const __grid_constant__ VerifyArgs a) {
-  constexpr int VF_WARPS = VF_THREADS / 32;
   __shared__ Rejected rj;
   __shared__ Sums sums;
   __shared__ double s_seg[VF_WARPS];  // sums of the warps' segments of the slice
@@ -383,12 +390,8 @@ extern "C" int ivc_verify_drafts(const float* p, long long p_ld, const float* q,
                      path, path_stride, n_path, next_token, static_cast<int*>(workspace)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   TraceScope ts("verify_drafts", s);
-  // Small vocabularies: one CTA. Otherwise wide CTAs while all clusters are
-  // resident with them (two per SM; one sequence 6.8 against 8.1 us), narrow ones
-  // beyond that (four per SM; 48 sequences without a rejection 12.9 against 16.0).
-  if (V <= VF_SMALL) return launch_k(verify_kernel<1, 384, 2>, dim3(B), dim3(384), 0, s, 1, a);
-  const unsigned ctas = static_cast<unsigned>(B) * VF_CLUSTER;
-  if (ctas <= 2u * num_sms())
-    return launch_k(verify_kernel<VF_CLUSTER, 384, 2>, dim3(ctas), dim3(384), 0, s, VF_CLUSTER, a);
-  return launch_k(verify_kernel<VF_CLUSTER, 256, 4>, dim3(ctas), dim3(256), 0, s, VF_CLUSTER, a);
+  // small vocabularies: one CTA (no cluster to wait for)
+  if (V <= VF_SMALL) return launch_k(verify_kernel<1>, dim3(B), dim3(VF_THREADS), 0, s, 1, a);
+  return launch_k(verify_kernel<VF_CLUSTER>, dim3(static_cast<unsigned>(B) * VF_CLUSTER),
+                  dim3(VF_THREADS), 0, s, VF_CLUSTER, a);
 }
