@@ -91,7 +91,34 @@ __device__ __forceinline__ int pieces_of(long long total, int grid) {
 __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
 
 // ------------------------------------------------------------------ plan
+// Sequence b as {first row, nodes, committed tokens, sequence}, all 0 where there
+// is nothing to do, and the DEV_* bits of what is wrong with it.
+__device__ __forceinline__ int4 seq_info(const ivc_cache& c, const TreeArgs& a, int b, int& bad) {
+  const int row = a.offsets[b], n = a.offsets[b + 1] - row;
+  const int4 none = make_int4(0, 0, 0, 0);
+  if (b == 0 && row != 0) bad |= DEV_BAD_TREE;
+  if (row < 0 || n < 0 || n > IVC_MAX_TREE || row > a.N - n) {
+    bad |= DEV_BAD_TREE;
+    return none;
+  }
+  if (n == 0) return none;
+  const int s = a.seqs ? a.seqs[b] : b;
+  const bool in = s >= 0 && s < c.max_seqs;
+  const int len = in ? c.length[s] : -1, np = in ? c.n_pages[s] : 0;
+  if (len < 0 || np > c.max_pages ||
+      static_cast<long long>(len) + n > static_cast<long long>(np) * c.page_tokens) {
+    bad |= DEV_BAD_CACHE;
+    return none;
+  }
+  return make_int4(row, n, len, s);
+}
+__device__ __forceinline__ long long tiles_of(const ivc_cache& c, const TreeArgs& a, const int4& info) {
+  return static_cast<long long>(div_up(info.z + info.y, TA_KEYS)) * c.kv_heads *
+         div_up(info.y, 2 * a.npt);
+}
+
 // One CTA: which tiles there are, and the sequence in which each piece begins.
+// (Batches of up to 32 sequences do without this kernel: see Walk.)
 __global__ void __launch_bounds__(1024)
     tree_plan_kernel(const __grid_constant__ ivc_cache c, const __grid_constant__ TreeArgs a,
                      int grid) {
@@ -103,29 +130,12 @@ __global__ void __launch_bounds__(1024)
   const int per = div_up(a.B, 1024);
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
   long long mine = 0;
-  int bad = tid == 0 && a.offsets[0] != 0 ? DEV_BAD_TREE : 0;
+  int bad = 0;
   for (int b = b0; b < b1; ++b) {
-    const int row = a.offsets[b], n = a.offsets[b + 1] - row;
-    int4 info = make_int4(0, 0, 0, 0);
-    long long tiles = 0;
-    if (row < 0 || n < 0 || n > IVC_MAX_TREE || row > a.N - n) {
-      bad |= DEV_BAD_TREE;
-    } else if (n > 0) {
-      const int s = a.seqs ? a.seqs[b] : b;
-      const bool in = s >= 0 && s < c.max_seqs;
-      const int len = in ? c.length[s] : -1, np = in ? c.n_pages[s] : 0;
-      if (len < 0 || np > c.max_pages ||
-          static_cast<long long>(len) + n > static_cast<long long>(np) * c.page_tokens) {
-        bad |= DEV_BAD_CACHE;
-      } else {
-        info = make_int4(row, n, len, s);
-        tiles = static_cast<long long>(div_up(len + n, TA_KEYS)) * c.kv_heads *
-                div_up(n, 2 * a.npt);
-      }
-    }
+    const int4 info = seq_info(c, a, b, bad);
     a.info[b] = info;
     s_prefix[b] = mine;  // within the thread; completed below
-    mine += tiles;
+    mine += tiles_of(c, a, info);
   }
   if (bad) atomicOr(a.status, bad);
   long long incl = mine;
@@ -150,7 +160,6 @@ __global__ void __launch_bounds__(1024)
   const long long total = s_prefix[a.B];
   const int pieces = pieces_of(total, grid);
   for (int i = tid; i < grid; i += 1024) {
-    a.head[2 * i] = make_int4(0, 0, 0, 0);
     if (i >= pieces) continue;
     const long long pos = total * i / pieces;  // the last sequence that begins at or before it
     int lo = 0, hi = a.B;
@@ -177,27 +186,61 @@ struct Item {
 // Walks a CTA's piece; every role of the CTA walks it for itself. Only the first
 // item is found by division; the ones after it are the next head, block of nodes
 // or sequence, whose info is read one sequence ahead.
+//
+// A batch of up to 32 sequences is planned by each warp for itself, lane b holding
+// sequence b: a kernel less in the stream (4 of 14 us for one short sequence).
 struct Walk {
   long long left;         // tiles of the piece not walked yet
+  long long total;        // of all pieces
   int b, q, t0;           // sequence, item of the sequence (block * kv_heads + head), tile
   int4 info, ahead;       // of sequences b and b + 1
+  int4 lane_info;         // of sequence `lane`, small batches
   __device__ int4 info_of(const TreeArgs& a, int s) const {
-    return s < a.B ? a.info[s] : make_int4(0, 0, 0, 0);
+    if (a.B > 32) return s < a.B ? a.info[s] : make_int4(0, 0, 0, 0);
+    const unsigned all = 0xffffffffu;  // lanes behind the batch hold 0
+    return s < 32 ? make_int4(__shfl_sync(all, lane_info.x, s), __shfl_sync(all, lane_info.y, s),
+                              __shfl_sync(all, lane_info.z, s), __shfl_sync(all, lane_info.w, s))
+                  : make_int4(0, 0, 0, 0);
   }
-  __device__ Walk(const TreeArgs& a) {
-    const long long total = a.prefix[a.B];
-    const int pieces = pieces_of(total, gridDim.x), i = blockIdx.x;
+  // By a whole warp, as next() is. `status`: null but in one warp of the grid.
+  __device__ Walk(const ivc_cache& c, const TreeArgs& a, int* status) {
+    const int i = blockIdx.x;
+    long long pos = 0, first = 0;
+    lane_info = make_int4(0, 0, 0, 0);
     left = 0;
+    if (a.B > 32) {
+      total = a.prefix[a.B];
+    } else {
+      const int lane = threadIdx.x & 31;
+      int bad = 0;
+      if (lane < a.B) lane_info = seq_info(c, a, lane, bad);
+      if (bad && status != nullptr) atomicOr(status, bad);
+      const long long mine = tiles_of(c, a, lane_info);
+      long long incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+      }
+      total = __shfl_sync(0xffffffffu, incl, 31);
+      const int pieces = pieces_of(total, gridDim.x);
+      if (i < pieces) pos = total * i / pieces;
+      b = min(31, __popc(__ballot_sync(0xffffffffu, incl <= pos)));  // the first that ends behind it
+      first = __shfl_sync(0xffffffffu, incl - mine, b);
+    }
+    const int pieces = pieces_of(total, gridDim.x);
     if (i >= pieces) return;
-    const long long pos = total * i / pieces;
+    if (a.B > 32) {
+      pos = total * i / pieces;
+      b = a.start[i];
+      first = a.prefix[b];
+    }
     left = total * (i + 1) / pieces - pos;
-    b = a.start[i];
     info = info_of(a, b);
     ahead = info_of(a, b + 1);
     const int tiles = div_up(info.z + info.y, TA_KEYS);
-    const long long at = pos - a.prefix[b];
-    q = static_cast<int>(at / tiles);
-    t0 = static_cast<int>(at % tiles);
+    q = static_cast<int>((pos - first) / tiles);
+    t0 = static_cast<int>((pos - first) % tiles);
   }
   __device__ bool next(const ivc_cache& c, const TreeArgs& a, Item& it) {
     if (left <= 0) return false;
@@ -433,7 +476,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
     const int pt = c.page_tokens, box = min(pt, TA_KEYS), per_tile = TA_KEYS / box;
     const int pt_log = 31 - __clz(pt), box_log = 31 - __clz(box);
     const int nowhere = c.pages * c.kv_heads * pt;  // behind the last row: reads as 0
-    Walk walk(a);
+    Walk walk(c, a, keys && blockIdx.x == 0 ? a.status : nullptr);
     Item it = {};
     int slot = 0, round = 0, queries = 0;
     // rows of the boxes (a page or half of one) of an item: lane l holds those of
@@ -515,7 +558,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
     const uint32_t idesc_o = idesc_bf16_f32(128, D) | (1u << 16);  // B MN-major
     const uint64_t kdesc = sw128_kmajor_desc(smem_u32(kring));
     const uint64_t vdesc = sw128_mnmajor_desc(smem_u32(vring), TA_HALF);
-    Walk walk(a);
+    Walk walk(c, a, nullptr);
     Item it = {};
     int items = 0, mends = 0, queries = 0;
     int ks = 0, kround = 0, vs = 0, vround = 0;  // the next tile's slots
@@ -652,8 +695,12 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t to = tmem + lanes + 256 + 128 * g;
     const int first_lane_row = quad * 32;
-    Walk walk(a);
+    Walk walk(c, a, nullptr);
     Item it = {};
+    if (threadIdx.x == 0) {  // for the merge
+      a.head[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+      if (blockIdx.x == 0 && a.B <= 32) a.prefix[a.B] = walk.total;
+    }
     int items = 0, nml = 0, sums = 0;  // sums: weighted sums asked for by this group
     uint32_t ns = 0;                   // bit buffer: phase of the scores
     while (ok && walk.next(c, a, it)) {
@@ -983,7 +1030,7 @@ int run_tree(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm
              const ivc_cache& c, const TreeArgs& a, int grid, cudaStream_t s) {
   const void* kern = reinterpret_cast<const void*>(tree_attend_kernel<D>);
   if (const int rc = smem_optin(kern, TaSmem<D>::TOTAL)) return rc;
-  {
+  if (a.B > 32) {
     TraceScope ts("tree.plan", s);
     if (const int rc = launch_k(tree_plan_kernel, dim3(1), dim3(1024), 0, s, 1, c, a, grid)) return rc;
   }
