@@ -695,6 +695,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t to = tmem + lanes + 256 + 128 * g;
     const int first_lane_row = quad * 32;
+    const int row_node = r / a.group, row_head = r - row_node * a.group;  // within a block of rows
     Walk walk(c, a, nullptr);
     Item it = {};
     if (threadIdx.x == 0) {  // for the merge
@@ -709,9 +710,11 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
       const int gnodes = min(a.npt, it.node0 + it.nodes - node0);
       const int rows = gnodes * a.group;
       const bool live = first_lane_row < rows;                        // the warp has rows
-      const int node = node0 + r / a.group;
+      const int node = node0 + row_node;
       uint32_t anc[4] = {0u, 0u, 0u, 0u};
-      if (live && it.t1 * TA_KEYS > it.len) {
+      if (it.n == 1) {
+        anc[0] = 1u;
+      } else if (live && it.t1 * TA_KEYS > it.len) {
         // parents of nodes 4 lane .. 4 lane + 3 in the bytes of one register
         uint32_t packed = 0;
         bool bad = false;
@@ -847,7 +850,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
         const int slot = 2 * blockIdx.x + (it.begins ? 1 : 0);
         const int prow = (it.rows2 ? g * TA_ROWS : 0) + r;
         bf16* dst = a.out + (static_cast<long long>(it.row + node) * a.q_heads +
-                             it.h * a.group + r % a.group) * D;
+                             it.h * a.group + row_head) * D;
         float4* part = a.part_o + static_cast<size_t>(slot) * (D / 4) * 256 + prow;
         const bool odd = it.t1 * TA_KEYS > it.len && (s_odd[items & 1][0] | s_odd[items & 1][1]) != 0;
 #pragma unroll 1
