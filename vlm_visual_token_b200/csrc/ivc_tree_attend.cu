@@ -94,7 +94,11 @@ __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
 // Sequence b as {first row, nodes, committed tokens, sequence}, all 0 where there
 // is nothing to do, and the DEV_* bits of what is wrong with it.
 __device__ __forceinline__ int4 seq_info(const ivc_cache& c, const TreeArgs& a, int b, int& bad) {
+  // (all loads at once: a kernel's first tile waits for them)
   const int row = a.offsets[b], n = a.offsets[b + 1] - row;
+  const int s = a.seqs ? a.seqs[b] : b;
+  const bool in = s >= 0 && s < c.max_seqs;
+  const int len = in ? c.length[s] : -1, np = in ? c.n_pages[s] : 0;
   const int4 none = make_int4(0, 0, 0, 0);
   if (b == 0 && row != 0) bad |= DEV_BAD_TREE;
   if (row < 0 || n < 0 || n > IVC_MAX_TREE || row > a.N - n) {
@@ -102,9 +106,6 @@ __device__ __forceinline__ int4 seq_info(const ivc_cache& c, const TreeArgs& a, 
     return none;
   }
   if (n == 0) return none;
-  const int s = a.seqs ? a.seqs[b] : b;
-  const bool in = s >= 0 && s < c.max_seqs;
-  const int len = in ? c.length[s] : -1, np = in ? c.n_pages[s] : 0;
   if (len < 0 || np > c.max_pages ||
       static_cast<long long>(len) + n > static_cast<long long>(np) * c.page_tokens) {
     bad |= DEV_BAD_CACHE;
@@ -375,29 +376,38 @@ template <int D>
 __device__ void mend_values(uint8_t* v, int base, int len, int n, int page_tokens, int* odd, int lane) {
   const int drafted = max(0, len - base), behind = min(TA_KEYS, len + n - base);
   const int end = min(TA_KEYS, div_up(len + n, page_tokens) * page_tokens - base);
+  constexpr int HALVES = D / 64, BATCH = 4;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  auto piece = [&](int i, int hf) {
+    return reinterpret_cast<uint4*>(v + hf * TA_HALF + (i >> 3) * 128 + (i & 7) * 16);
+  };
+  for (int i = behind * 8 + lane; i < end * 8; i += 32)
+#pragma unroll
+    for (int hf = 0; hf < HALVES; ++hf) *piece(i, hf) = zero;
   bool found = false;
-  for (int i = lane; i < (end - drafted) * 8; i += 32) {
-    const int r = drafted + (i >> 3);
+  for (int i0 = drafted * 8 + lane; i0 < behind * 8; i0 += 32 * BATCH) {
+    uint4 x[BATCH][HALVES];  // all loads of a batch before the first test
 #pragma unroll
-    for (int hf = 0; hf < D / 64; ++hf) {
-      uint4* at = reinterpret_cast<uint4*>(v + hf * TA_HALF + r * 128 + (i & 7) * 16);
-      if (r >= behind) {
-        *at = make_uint4(0u, 0u, 0u, 0u);
-        continue;
-      }
-      uint4 x = *at;
-      uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-      bool here = false;
+    for (int k = 0; k < BATCH; ++k)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if ((w[j] & 0x7f80u) == 0x7f80u) { w[j] &= 0xffff0000u; here = true; }
-        if ((w[j] & 0x7f800000u) == 0x7f800000u) { w[j] &= 0x0000ffffu; here = true; }
+      for (int hf = 0; hf < HALVES; ++hf)
+        x[k][hf] = i0 + 32 * k < behind * 8 ? *piece(i0 + 32 * k, hf) : zero;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k)
+#pragma unroll
+      for (int hf = 0; hf < HALVES; ++hf) {
+        uint32_t w[4] = {x[k][hf].x, x[k][hf].y, x[k][hf].z, x[k][hf].w};
+        bool here = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if ((w[j] & 0x7f80u) == 0x7f80u) { w[j] &= 0xffff0000u; here = true; }
+          if ((w[j] & 0x7f800000u) == 0x7f800000u) { w[j] &= 0x0000ffffu; here = true; }
+        }
+        if (here) {
+          *piece(i0 + 32 * k, hf) = make_uint4(w[0], w[1], w[2], w[3]);
+          found = true;
+        }
       }
-      if (here) {
-        *at = x;
-        found = true;
-      }
-    }
   }
   if (found) *odd = 1;
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
