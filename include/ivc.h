@@ -13,7 +13,9 @@
  *     learnable query refined by 4 masked multi-head cross-attention layers
  *     over each tile's tokens), Gating (4 residual MLP blocks, Linear(D,2),
  *     softmax), the double threshold gate > quantile_0.1(gate of the image)
- *     AND gate >= 0.5, and compaction of every tile to 64 or 256 rows.
+ *     AND gate >= 0.5, and compaction of every tile to 64 or 256 rows;
+ *   - the splice of those rows into the token sequences, and behind it the
+ *     operators of a decode step over a paged cache.
  *
  * Sources, by page title and section:
  *   [PS]  InternVL3-14B-Instruct, "Pixel Shuffle + MLP connector, line by line":

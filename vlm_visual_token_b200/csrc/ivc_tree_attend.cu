@@ -14,7 +14,8 @@
 //     contiguous piece of the list of all (sequence, row block, kv head, tile):
 //     long and short sequences are cut wherever the pieces end, and the parts of
 //     a cut item are merged by a second kernel in part order;
-//   - keys and values come by TMA, one box per page, into a ring of 160 KB;
+//   - keys and values come by TMA, one box per page and 64 values, into rings of
+//     80 KB each;
 //   - two groups of four softmax warps keep the tensor core and the exponential
 //     unit busy at the same time: with more than 128 query rows each group has
 //     128 rows and every tile; with fewer (plain decoding) both have the same
@@ -28,6 +29,10 @@
 // 237 us. O stays in TMEM; it is rescaled only when a row's maximum rose by more
 // than 2^8 (p then reaches 2^8 at most, which bf16 and the fp32 sums hold as
 // exactly as values below 1).
+//
+// 48 sequences of up to 4500 tokens, one node: 135 us (705 MB, 5.2 TB/s); 24 of up to
+// 6000 with 27 nodes: 120 us; 4 of up to 40800 with 64 nodes: 191 us, there bound by the
+// MMAs (N = 64 takes as long as N = 128), not by HBM.
 //
 // Rounding: p to bf16 for the product with v (the sum l takes the unrounded p);
 // everything else is fp32 until the output.
