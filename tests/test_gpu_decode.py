@@ -435,6 +435,9 @@ def test_tree_attention_bad_device_data():
     assert st == BAD and torch.equal(out[:6], good[:6]) and (out[6:] == 7).all()
     out, st = run(None, [0, 12, 6])
     assert st & 128
+    lone = ivc.tree_attention(p.gpu, 0, q[:2], None, dev([0, 1, 2]))
+    out, st = run(dev([0, -1]), [0, 1, 2], qq=q[:2])                  # a single node with a parent
+    assert st == 128 and torch.equal(out, lone)
     big = torch.randn(140, 4, 64, dtype=torch.bfloat16, device="cuda")
     out, st = run(None, [0, 6, 140], qq=big)                          # more than 128 nodes
     assert st & 128 and (out[6:] == 7).all() and torch.isfinite(out[:6].float()).all()

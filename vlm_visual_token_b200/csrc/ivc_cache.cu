@@ -491,6 +491,7 @@ __global__ void __launch_bounds__(CA_THREADS)
 // tokens of three sequences in 36 layers, 0.7 GB read and written, take 145 us.
 constexpr int MV_THREADS = 256;
 constexpr int MV_PIECES = 4;  // 16-byte pieces a thread holds of a chunk
+constexpr int MV_CTAS = 8;
 __global__ void __launch_bounds__(MV_THREADS, 4)
     cache_move_kernel(ivc_cache c, CompactPlan plan, int stride, int head_groups,
                       int heads_per_group) {
@@ -687,12 +688,16 @@ int ivc_cache_compact(const ivc_cache* c, const int32_t* count, const int32_t* k
     if (rc != IVC_OK) return rc;
   }
   if (stride == 0) return IVC_OK;
-  // two of a CTA's chunks are 2 * MV_PIECES * MV_THREADS pieces: few kept tokens share a CTA over
-  // several heads, many get a CTA per head. (A sequence's tokens are at most
-  // pages * page_tokens <= 2^27, 16 pieces each, and only strides of at most one
-  // chunk share a CTA, so a CTA's pieces are counted in 32 bits.)
-  const int per_chunk = 2 * MV_PIECES * MV_THREADS / (c->head_dim / 8);
-  int per_group = per_chunk / stride;
+  // A CTA takes as many heads as leaves MV_CTAS CTAs per SM. (Not by the keep
+  // lists' width, which says little of the counts: for 48 paths of 7 tokens in lists
+  // 128 wide, reserve and compact took 79 us with a CTA per head and take 42.) 4 per
+  // SM: 697 against 670 us for the thinned prefixes; 16: the same. A sequence's tokens are at most
+  // pages * page_tokens <= 2^27, and a head 16 pieces; more heads than one only
+  // where that stays in 32 bits.
+  const long long planes = 2ll * n * c->layers, wanted = MV_CTAS * num_sms();
+  int per_group = static_cast<int>(c->kv_heads * planes / wanted);
+  const long long most = (1ll << 31) / 16 / (static_cast<long long>(c->pages) * c->page_tokens);
+  if (per_group > most) per_group = static_cast<int>(most);
   per_group = per_group < 1 ? 1 : per_group > c->kv_heads ? c->kv_heads : per_group;
   const int groups = (c->kv_heads + per_group - 1) / per_group;
   TraceScope ts("cache.move", s);

@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
   __shared__ __align__(8) uint64_t vfull[S::SLOTS], vempty[S::SLOTS];
   __shared__ __align__(8) uint64_t qfull[2], qempty[2];  // of each 128-row buffer
   __shared__ __align__(8) uint64_t sfull[2][2], pready[2][2], odone[2];  // [group][S buffer]
-  __shared__ __align__(8) uint64_t ofull, ofree, mlready, mended, seen;
+  __shared__ __align__(8) uint64_t ofull, ofree, mlready, mended, seen, drained[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_odd[2][2];       // [item & 1][issuer]: a drafted value is not finite
   __shared__ float2 s_ml[TA_ROWS];  // group 1's maximum and sum
@@ -454,6 +454,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
         mbar_init(&pready[g][buf], 4);
       }
       mbar_init(&odone[g], 1);
+      mbar_init(&drained[g], 1);
       mbar_init(&qfull[g], 1);
       mbar_init(&qempty[g], 2);
     }
@@ -554,6 +555,10 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
           ++round;
         }
       }
+      // a single node has no parent to walk to; whether it names one is looked up here
+      if (!keys && it.n == 1 && it.h == 0 && it.begins && lane == 0 && a.parents != nullptr &&
+          a.parents[it.row] != -1)
+        atomicOr(a.status, DEV_BAD_TREE);
     }
     if (!ok) {  // let the copies in flight land
       const int loads = round * S::SLOTS + slot;
@@ -702,6 +707,11 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
         if (more) advance(ks, kround);
       }
       ++items;
+    }
+    if (!ok) {  // let the MMAs in flight end before the TMEM is given back
+      if (elect_one()) umma_commit(&drained[g]);
+      __syncwarp();
+      warp_wait(&drained[g], 0);
     }
   } else if (warp < 8) {
     // ------------------------------------------------------ softmax, epilogue

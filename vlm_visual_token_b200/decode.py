@@ -104,6 +104,8 @@ def _on(device, stream):
     if device.type != "cuda":
         _refuse("the tensors are not on a GPU")
     if stream is not None:
+        if stream.device != device:
+            _refuse("stream: it is another device's")
         return _other(device, stream)
     return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
