@@ -72,13 +72,14 @@ def _refuse(what: str, code: int = -1):
 
 def _need(t, what: str, dtype, dims: int, device, n: int = -1) -> int:
     """t is a dense tensor of this type, rank and device (with n values); its address."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != dims or t.device != device:
-        _refuse(f"{what}: a {dims}-dimensional {dtype} tensor on {device} is needed")
-    if not t.is_contiguous():
-        _refuse(f"{what}: not contiguous")
-    if n >= 0 and t.numel() != n:
-        _refuse(f"{what}: {n} values are needed")
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.dim() == dims and t.device == device and t.is_contiguous() and \
+                (n < 0 or t.numel() == n):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    count = f" of {n} values" if n >= 0 else ""
+    _refuse(f"{what}: a contiguous {dims}-dimensional {dtype} tensor{count} on {device} is needed")
 
 
 def _maybe(t, what: str, dtype, dims: int, device, n: int = -1) -> Optional[int]:
@@ -95,22 +96,21 @@ def _rows(t, what: str, dtype, device) -> int:
     return t.stride(0) if rows > 1 else max(width, 1)
 
 
+# (the public forms build objects and take over a microsecond of each call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _on(device, stream):
-    """Makes `device` and `stream` current for a call, where they are not."""
-    if device.type != "cuda":
-        _refuse("the tensors are not on a GPU")
+def _elsewhere(device, stream):
+    """None where a call can run as it is; else the context to repeat it in, which
+    makes `device` and `stream` current."""
     if stream is not None:
         if stream.device != device:
             _refuse("stream: it is another device's")
         return _other(device, stream)
-    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-
-_HERE = contextlib.nullcontext()
+    index = device.index  # None: not a GPU, which _call refuses
+    return None if index is None or index == _current_device() else torch.cuda.device(device)
 
 
 @contextlib.contextmanager
@@ -120,6 +120,8 @@ def _other(device, stream):
 
 
 def _call(name: str, device, *args) -> None:
+    if device.index is None:
+        _refuse(f"{name}: the tensors are not on a GPU")
     ivc = _pkg()
     rc = getattr(ivc._LIB, name)(*args, _raw_stream(device.index))
     if rc != 0:
@@ -172,7 +174,7 @@ class Cache:
         dev = torch.device(device)
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
-        with _on(dev, stream):
+        with _elsewhere(dev, stream) or contextlib.nullcontext():
             shape = (layers, pages, kv_heads, page_tokens, head_dim)
             k, v = (torch.empty(shape, dtype=torch.bfloat16, device=dev) for _ in range(2))
             ints = [torch.empty(s, dtype=torch.int32, device=dev)
@@ -195,12 +197,15 @@ def cache_reserve(cache: Cache, tokens: torch.Tensor, seqs: Optional[torch.Tenso
                   workspace=None, stream=None) -> None:
     """Pages for tokens[i] more tokens of sequence seqs[i] (default: i)."""
     dev = cache.device
+    other = _elsewhere(dev, stream)
+    if other is not None:
+        with other:
+            return cache_reserve(cache, tokens, seqs, workspace)
     t = _need(tokens, "tokens", torch.int32, 1, dev)
     n = tokens.shape[0]
     s = _maybe(seqs, "seqs", torch.int32, 1, dev, n)
-    with _on(dev, stream):
-        ws = _workspace(workspace, STEP_WORKSPACE_BYTES, dev)
-        _call("ivc_cache_reserve", dev, cache._p, t, s, n, ws.data_ptr(), ws.shape[0])
+    ws = _workspace(workspace, STEP_WORKSPACE_BYTES, dev)
+    _call("ivc_cache_reserve", dev, cache._p, t, s, n, ws.data_ptr(), ws.shape[0])
 
 
 def cache_fork(cache: Cache, src: torch.Tensor, dst: torch.Tensor, share: bool = True,
@@ -208,12 +213,15 @@ def cache_fork(cache: Cache, src: torch.Tensor, dst: torch.Tensor, share: bool =
     """Empty sequence dst[i] becomes a copy of src[i]: its full pages shared, or
     (share=False) every page copied."""
     dev = cache.device
+    other = _elsewhere(dev, stream)
+    if other is not None:
+        with other:
+            return cache_fork(cache, src, dst, share, workspace)
     a = _need(src, "src", torch.int32, 1, dev)
     n = src.shape[0]
     b = _need(dst, "dst", torch.int32, 1, dev, n)
-    with _on(dev, stream):
-        ws = _workspace(workspace, 0 if workspace is not None else cache_workspace_size(cache, n), dev)
-        _call("ivc_cache_fork", dev, cache._p, a, b, n, 1 if share else 0, ws.data_ptr(), ws.shape[0])
+    ws = _workspace(workspace, 0 if workspace is not None else cache_workspace_size(cache, n), dev)
+    _call("ivc_cache_fork", dev, cache._p, a, b, n, 1 if share else 0, ws.data_ptr(), ws.shape[0])
 
 
 def cache_compact(cache: Cache, count: torch.Tensor, keep: Optional[torch.Tensor] = None,
@@ -223,6 +231,10 @@ def cache_compact(cache: Cache, count: torch.Tensor, keep: Optional[torch.Tensor
     the last of them the sequence's last (keep None: the first count[i]; start
     None: the committed length). Pages behind that are freed."""
     dev = cache.device
+    other = _elsewhere(dev, stream)
+    if other is not None:
+        with other:
+            return cache_compact(cache, count, keep, start, seqs, workspace)
     m = _need(count, "count", torch.int32, 1, dev)
     n = count.shape[0]
     k, width = None, 0
@@ -234,19 +246,21 @@ def cache_compact(cache: Cache, count: torch.Tensor, keep: Optional[torch.Tensor
         k = k or m  # rows of no tokens have no address; none of them is read
     a = _maybe(start, "start", torch.int32, 1, dev, n)
     s = _maybe(seqs, "seqs", torch.int32, 1, dev, n)
-    with _on(dev, stream):
-        ws = _workspace(workspace, 0 if workspace is not None else cache_workspace_size(cache, n, width),
-                        dev)
-        _call("ivc_cache_compact", dev, cache._p, m, k, width, a, s, n, ws.data_ptr(), ws.shape[0])
+    ws = _workspace(workspace, 0 if workspace is not None else cache_workspace_size(cache, n, width),
+                    dev)
+    _call("ivc_cache_compact", dev, cache._p, m, k, width, a, s, n, ws.data_ptr(), ws.shape[0])
 
 
 def cache_free(cache: Cache, seqs: torch.Tensor, workspace=None, stream=None) -> None:
     """The sequences become empty; pages that no other sequence holds are freed."""
     dev = cache.device
+    other = _elsewhere(dev, stream)
+    if other is not None:
+        with other:
+            return cache_free(cache, seqs, workspace)
     s = _need(seqs, "seqs", torch.int32, 1, dev)
-    with _on(dev, stream):
-        ws = _workspace(workspace, STEP_WORKSPACE_BYTES, dev)
-        _call("ivc_cache_free", dev, cache._p, s, seqs.shape[0], ws.data_ptr(), ws.shape[0])
+    ws = _workspace(workspace, STEP_WORKSPACE_BYTES, dev)
+    _call("ivc_cache_free", dev, cache._p, s, seqs.shape[0], ws.data_ptr(), ws.shape[0])
 
 
 def _out(out, N: int, q_heads: int, D: int, device):
@@ -266,6 +280,11 @@ def qk_norm_rope(cache: Cache, layer: int, qkv: torch.Tensor, q_gamma: torch.Ten
     kv_heads) * head_dim] (rows may be strided); keys and values go to the cache
     behind the committed tokens, the queries [N, q_heads, head_dim] are returned."""
     dev, D = cache.device, cache.head_dim
+    other = _elsewhere(dev, stream)
+    if other is not None:
+        with other:
+            return qk_norm_rope(cache, layer, qkv, q_gamma, k_gamma, positions, offsets, theta, eps,
+                                seqs, out, workspace)
     ld = _rows(qkv, "qkv", torch.bfloat16, dev)
     N, width = qkv.shape
     heads, rest = divmod(width, D)
@@ -278,18 +297,17 @@ def qk_norm_rope(cache: Cache, layer: int, qkv: torch.Tensor, q_gamma: torch.Ten
     off = _need(offsets, "offsets", torch.int32, 1, dev)
     B = offsets.shape[0] - 1
     s = _maybe(seqs, "seqs", torch.int32, 1, dev, B)
-    with _on(dev, stream):
-        out = _out(out, N, q_heads, D, dev)
-        ws = _workspace(workspace, STEP_WORKSPACE_BYTES, dev)
-        _call("ivc_qk_norm_rope", dev, cache._p, layer, qkv.data_ptr(), ld, N, q_heads, gq, gk, eps,
-              theta, pos, off, s, B, out.data_ptr(), ws.data_ptr(), ws.shape[0])
+    out = _out(out, N, q_heads, D, dev)
+    ws = _workspace(workspace, STEP_WORKSPACE_BYTES, dev)
+    _call("ivc_qk_norm_rope", dev, cache._p, layer, qkv.data_ptr(), ld, N, q_heads, gq, gk, eps,
+          theta, pos, off, s, B, out.data_ptr(), ws.data_ptr(), ws.shape[0])
     return out
 
 
 def tree_attention_workspace_size(cache: Cache, N: int, q_heads: int, B: int) -> int:
     """Bytes that tree_attention needs for N rows of q_heads heads in B sequences."""
     ivc = _pkg()
-    with _on(cache.device, None):
+    with _elsewhere(cache.device, None) or contextlib.nullcontext():
         size = ivc.lib().ivc_tree_attention_workspace_size(cache._p, N, q_heads, B)
     if size == 0:
         raise ivc.IvcError(-2, "ivc_tree_attention_workspace_size")
@@ -304,6 +322,10 @@ def tree_attention(cache: Cache, layer: int, q: torch.Tensor, parents: Optional[
     strided) over their committed tokens, ancestors and themselves. parents None:
     chains. scale: 1 / sqrt(head_dim) by default."""
     dev, D = cache.device, cache.head_dim
+    other = _elsewhere(dev, stream)
+    if other is not None:
+        with other:
+            return tree_attention(cache, layer, q, parents, offsets, seqs, scale, out, workspace)
     if not isinstance(q, torch.Tensor) or q.dtype != torch.bfloat16 or q.dim() != 3 or \
             q.device != dev or q.shape[2] != D:
         _refuse(f"q: a bf16 tensor [N, q_heads, {D}] on {dev} is needed")
@@ -315,13 +337,12 @@ def tree_attention(cache: Cache, layer: int, q: torch.Tensor, parents: Optional[
     off = _need(offsets, "offsets", torch.int32, 1, dev)
     B = offsets.shape[0] - 1
     s = _maybe(seqs, "seqs", torch.int32, 1, dev, B)
-    with _on(dev, stream):
-        out = _out(out, N, q_heads, D, dev)
-        ws = _workspace(workspace, 0 if workspace is not None else
-                        tree_attention_workspace_size(cache, N, q_heads, B), dev)
-        _call("ivc_tree_attention", dev, cache._p, layer, q.data_ptr(), ld, N, q_heads,
-              D ** -0.5 if scale is None else scale, par, off, s, B, out.data_ptr(), ws.data_ptr(),
-              ws.shape[0])
+    out = _out(out, N, q_heads, D, dev)
+    ws = _workspace(workspace, 0 if workspace is not None else
+                    tree_attention_workspace_size(cache, N, q_heads, B), dev)
+    _call("ivc_tree_attention", dev, cache._p, layer, q.data_ptr(), ld, N, q_heads,
+          D ** -0.5 if scale is None else scale, par, off, s, B, out.data_ptr(), ws.data_ptr(),
+          ws.shape[0])
     return out
 
 
@@ -333,6 +354,10 @@ def verify_drafts(p: torch.Tensor, q: Optional[torch.Tensor], tokens: torch.Tens
     strided), q the probabilities they were drafted from, or None. Returns
     (path [B, path_width] int32, n_path [B], next_token [B])."""
     dev = p.device
+    other = _elsewhere(dev, stream)
+    if other is not None:
+        with other:
+            return verify_drafts(p, q, tokens, parents, offsets, u, u_next, out, path_width, workspace)
     p_ld = _rows(p, "p", torch.float32, dev)
     N, V = p.shape
     q_ld, q_at = 0, None
@@ -346,18 +371,17 @@ def verify_drafts(p: torch.Tensor, q: Optional[torch.Tensor], tokens: torch.Tens
     off = _need(offsets, "offsets", torch.int32, 1, dev)
     B = offsets.shape[0] - 1
     un = _need(u_next, "u_next", torch.float32, 1, dev, max(B, 0))
-    with _on(dev, stream):
-        if out is None:
-            out = (torch.empty(max(B, 0), path_width, dtype=torch.int32, device=dev),
-                   torch.empty(max(B, 0), dtype=torch.int32, device=dev),
-                   torch.empty(max(B, 0), dtype=torch.int32, device=dev))
-        path, n_path, token = out
-        at = _need(path, "path", torch.int32, 2, dev)
-        if path.shape[0] != B:
-            _refuse("path: one row for each sequence is needed")
-        m, t = _need(n_path, "n_path", torch.int32, 1, dev, B), _need(token, "next_token", torch.int32, 1,
-                                                                    dev, B)
-        ws = _workspace(workspace, STEP_WORKSPACE_BYTES, dev)
-        _call("ivc_verify_drafts", dev, p.data_ptr(), p_ld, q_at, q_ld, N, V, tok, par, off, B, uu, un,
-              at, path.shape[1], m, t, ws.data_ptr(), ws.shape[0])
+    if out is None:
+        out = (torch.empty(max(B, 0), path_width, dtype=torch.int32, device=dev),
+               torch.empty(max(B, 0), dtype=torch.int32, device=dev),
+               torch.empty(max(B, 0), dtype=torch.int32, device=dev))
+    path, n_path, token = out
+    at = _need(path, "path", torch.int32, 2, dev)
+    if path.shape[0] != B:
+        _refuse("path: one row for each sequence is needed")
+    m, t = _need(n_path, "n_path", torch.int32, 1, dev, B), _need(token, "next_token", torch.int32, 1,
+                                                                dev, B)
+    ws = _workspace(workspace, STEP_WORKSPACE_BYTES, dev)
+    _call("ivc_verify_drafts", dev, p.data_ptr(), p_ld, q_at, q_ld, N, V, tok, par, off, B, uu, un,
+          at, path.shape[1], m, t, ws.data_ptr(), ws.shape[0])
     return out
