@@ -30,7 +30,7 @@
 namespace ivc {
 namespace {
 
-constexpr int QR_THREADS = 256;
+constexpr int QR_THREADS = 128;
 constexpr int QR_WARPS = QR_THREADS / 32;
 constexpr int QR_LOADS = 4;  // heads of a batch, per lane
 
@@ -82,7 +82,7 @@ __device__ __forceinline__ int seq_of_row(const int32_t* offsets, int B, int tok
 }
 
 template <int D>
-__global__ void __launch_bounds__(QR_THREADS, 4)
+__global__ void __launch_bounds__(QR_THREADS, 8)
     qk_norm_rope_kernel(const __grid_constant__ ivc_cache c, const __grid_constant__ QkArgs a,
                         const __grid_constant__ RopeFreq freq) {
   constexpr int LANES = D / 8;               // lanes per head
