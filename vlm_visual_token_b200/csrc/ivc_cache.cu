@@ -25,14 +25,32 @@ constexpr int CA_WARPS = CA_THREADS / 32;
 constexpr int CA_MAX_SEQS = 65536;
 constexpr int CA_MAX_PAGES = 1 << 20;
 
-// What the plan kernels keep in shared memory besides the page bitmap.
+// What the plan kernels keep in shared memory besides the page bitmap. The
+// sequences of a call are taken in passes of CA_THREADS, a thread each; their pages
+// by all threads (see pages_of_pass).
 struct PlanShared {
   unsigned seen[CA_MAX_SEQS / 32];  // sequences named by this call
-  int order[CA_THREADS];            // one pass of sequences: pages before this one's
+  int seq[CA_THREADS];              // of this pass
+  int from[CA_THREADS];             // fork: the source; compact: the first token
+  int len[CA_THREADS];              // committed tokens; compact: tokens kept
+  int np[CA_THREADS];               // pages held
+  int order[CA_THREADS];            // pages taken before this sequence's
   int need[CA_THREADS];             // pages it takes
   long long warp_sum[CA_WARPS];
   int bad;                          // DEV_* bits
 };
+
+// Calls f(e, j) for every page j < count(e) of every sequence e < m of a pass: as
+// many neighbouring threads per sequence as there are, so that a few sequences'
+// pages and many sequences' are read in few dependent steps.
+template <typename Count, typename F>
+__device__ __forceinline__ void pages_of_pass(int m, Count count, F f) {
+  const int lanes = 1 << (31 - __clz(CA_THREADS / max(m, 1)));  // m * lanes <= CA_THREADS
+  const int e = threadIdx.x / lanes;
+  if (e >= m) return;
+  const int n = count(e);
+  for (int j = threadIdx.x % lanes; j < n; j += lanes) f(e, j);
+}
 
 // Exclusive sum over the CTA; every thread calls it. `total` gets the whole sum.
 __device__ long long block_scan(long long v, long long* s_warp, long long& total) {
@@ -78,38 +96,36 @@ __device__ int seq_sound(const ivc_cache& c, int s) {
 }
 __device__ __forceinline__ bool page_ok(const ivc_cache& c, int p) { return p >= 0 && p < c.pages; }
 
-__device__ void plan_begin(const ivc_cache& c, PlanShared& sh) {
+// The pages on the free list, once `seen` is clear.
+__device__ int plan_begin(const ivc_cache& c, PlanShared& sh) {
+  const int fc = *c.free_count;
   for (int i = threadIdx.x; i < (c.max_seqs + 31) / 32; i += CA_THREADS) sh.seen[i] = 0;
-  if (threadIdx.x == 0) {
-    const int fc = *c.free_count;
-    sh.bad = fc < 0 || fc > c.pages ? DEV_BAD_CACHE : 0;
-  }
+  if (threadIdx.x == 0) sh.bad = fc < 0 || fc > c.pages ? DEV_BAD_CACHE : 0;
   __syncthreads();
+  return fc;
 }
 
-// Hands out pages: this pass's sequence threadIdx.x takes need[threadIdx.x]
-// pages behind its n_pages, `taken` pages after the first one handed out by
-// this call. Warps take sequences, lanes their pages.
-__device__ void take_pages(const ivc_cache& c, PlanShared& sh, const int32_t* seqs, int base, int n,
-                           int free_count) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int e = warp; e < CA_THREADS && base + e < n; e += CA_WARPS) {
-    const int need = sh.need[e];
-    if (need == 0) continue;
-    const int s = seq_of(seqs, base + e);
-    const int have = c.n_pages[s];
-    int32_t* row = c.table + static_cast<size_t>(s) * c.max_pages + have;
-    for (int j = lane; j < need; j += 32) {
-      const int at = free_count - 1 - (sh.order[e] + j);
-      const int p = c.free_list[at];
-      c.free_list[at] = -1;
-      row[j] = p;
-      if (page_ok(c, p)) c.ref[p] = 1;
-      else atomicOr(&sh.bad, DEV_BAD_CACHE);
-    }
-    __syncwarp();
-    if (lane == 0) c.n_pages[s] = have + need;
+// Whether everything was sound so far: the same in every thread, and nobody sets
+// sh.bad before all have read it.
+__device__ bool still_good(const PlanShared& sh) {
+  __syncthreads();
+  const bool good = sh.bad == 0;
+  __syncthreads();
+  return good;
+}
+
+// The k-th page that this call takes off the free list; -1 (and DEV_BAD_CACHE) where
+// the list holds no page there.
+__device__ __forceinline__ int take_page(const ivc_cache& c, PlanShared& sh, int free_count, int k) {
+  const int at = free_count - 1 - k;
+  const int p = c.free_list[at];
+  c.free_list[at] = -1;
+  if (page_ok(c, p)) {
+    c.ref[p] = 1;
+    return p;
   }
+  atomicOr(&sh.bad, DEV_BAD_CACHE);
+  return -1;
 }
 
 // One holder less of page p; its bit is set when that was the last one.
@@ -178,45 +194,56 @@ __global__ void __launch_bounds__(CA_THREADS)
   __shared__ PlanShared sh;
   pdl_wait();
   pdl_trigger();
-  plan_begin(c, sh);
-  const int fc = *c.free_count;
-  // pages a sequence lacks for length + tokens[i] tokens
-  auto lacks = [&](int i, int s, int& bad) -> int {
-    if (tokens[i] < 0) { bad = DEV_BAD_CACHE; return 0; }
-    const long long want = (static_cast<long long>(c.length[s]) + tokens[i] + c.page_tokens - 1) /
-                           c.page_tokens;
-    if (want > c.max_pages) { bad = DEV_CACHE_FULL; return 0; }
-    return want > c.n_pages[s] ? static_cast<int>(want) - c.n_pages[s] : 0;
+  const int fc = plan_begin(c, sh);
+  const int tid = threadIdx.x;
+  // sequence base + tid: its number, pages, and the pages it lacks for length +
+  // tokens[] tokens, into shared memory
+  auto read = [&](int base, bool first_time) {
+    const int i = base + tid;
+    int bad = 0, s = 0, need = 0;
+    if (i < n) {
+      s = seq_of(seqs, i);
+      if (first_time) bad = claim_seq(c, sh, s);
+      if (!bad) bad = seq_sound(c, s);
+      if (!bad) {
+        const int np = c.n_pages[s];
+        const long long want =
+            (static_cast<long long>(c.length[s]) + tokens[i] + c.page_tokens - 1) / c.page_tokens;
+        if (tokens[i] < 0) bad = DEV_BAD_CACHE;
+        else if (want > c.max_pages) bad = DEV_CACHE_FULL;
+        else if (want > np) need = static_cast<int>(want) - np;
+        sh.np[tid] = np;
+      }
+      if (bad) atomicOr(&sh.bad, bad);
+    }
+    sh.seq[tid] = s;
+    sh.need[tid] = need;
+    return need;
   };
   long long need = 0, total;
-  for (int i = threadIdx.x; i < n; i += CA_THREADS) {
-    const int s = seq_of(seqs, i);
-    int bad = claim_seq(c, sh, s);
-    if (!bad) bad = seq_sound(c, s);
-    if (!bad) need += lacks(i, s, bad);
-    if (bad) atomicOr(&sh.bad, bad);
-  }
+  for (int base = 0; base < n; base += CA_THREADS) need += read(base, true);
   block_scan(need, sh.warp_sum, total);
-  if (threadIdx.x == 0 && total > fc) sh.bad |= DEV_CACHE_FULL;
-  __syncthreads();
-  if (sh.bad == 0 && total > 0) {
+  if (tid == 0 && total > fc) sh.bad |= DEV_CACHE_FULL;
+  if (still_good(sh) && total > 0) {
     long long carry = 0;
     for (int base = 0; base < n; base += CA_THREADS) {
-      const int i = base + threadIdx.x;
-      int ignored = 0;
-      const int mine = i < n ? lacks(i, seq_of(seqs, i), ignored) : 0;
+      if (n > CA_THREADS) read(base, false);
+      const int m = min(CA_THREADS, n - base);
       long long sum;
-      sh.order[threadIdx.x] = static_cast<int>(carry + block_scan(mine, sh.warp_sum, sum));
-      sh.need[threadIdx.x] = mine;
+      sh.order[tid] = static_cast<int>(carry + block_scan(sh.need[tid], sh.warp_sum, sum));
       __syncthreads();
-      take_pages(c, sh, seqs, base, n, fc);
+      pages_of_pass(m, [&](int e) { return sh.need[e]; }, [&](int e, int j) {
+        c.table[static_cast<size_t>(sh.seq[e]) * c.max_pages + sh.np[e] + j] =
+            take_page(c, sh, fc, sh.order[e] + j);
+      });
+      if (tid < m && sh.need[tid] > 0) c.n_pages[sh.seq[tid]] = sh.np[tid] + sh.need[tid];
       carry += sum;
       __syncthreads();
     }
-    if (threadIdx.x == 0) *c.free_count = fc - static_cast<int>(total);
+    if (tid == 0) *c.free_count = fc - static_cast<int>(total);
   }
   __syncthreads();
-  if (threadIdx.x == 0 && sh.bad) atomicOr(status, sh.bad);
+  if (tid == 0 && sh.bad) atomicOr(status, sh.bad);
 }
 
 __global__ void __launch_bounds__(CA_THREADS)
@@ -227,32 +254,38 @@ __global__ void __launch_bounds__(CA_THREADS)
   pdl_trigger();
   plan_begin(c, sh);
   clear_freed(c, freed);
-  for (int i = threadIdx.x; i < n; i += CA_THREADS) {
+  const int tid = threadIdx.x;
+  auto read = [&](int base, bool first_time) {
+    const int i = base + tid;
+    if (i >= n) return;
     const int s = seq_of(seqs, i);
-    int bad = claim_seq(c, sh, s);
+    int bad = first_time ? claim_seq(c, sh, s) : 0;
     if (!bad) bad = seq_sound(c, s);
-    if (bad) atomicOr(&sh.bad, bad);
-  }
-  __syncthreads();
-  if (sh.bad == 0) {
-    __syncthreads();  // drop_page may set bad: nobody decides by it any more
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int i = warp; i < n; i += CA_WARPS) {
-      const int s = seq_of(seqs, i);
-      const int np = c.n_pages[s];
-      int32_t* row = c.table + static_cast<size_t>(s) * c.max_pages;
-      for (int j = lane; j < np; j += 32) {
-        drop_page(c, sh, freed, row[j]);
-        row[j] = -1;
-      }
-      __syncwarp();
-      if (lane == 0) c.n_pages[s] = c.length[s] = 0;
+    if (bad) {
+      atomicOr(&sh.bad, bad);
+      return;
     }
-    __syncthreads();
+    sh.seq[tid] = s;
+    sh.np[tid] = c.n_pages[s];
+  };
+  for (int base = 0; base < n; base += CA_THREADS) read(base, true);
+  if (still_good(sh)) {
+    for (int base = 0; base < n; base += CA_THREADS) {
+      if (n > CA_THREADS) read(base, false);
+      __syncthreads();
+      const int m = min(CA_THREADS, n - base);
+      pages_of_pass(m, [&](int e) { return sh.np[e]; }, [&](int e, int j) {
+        int32_t* at = c.table + static_cast<size_t>(sh.seq[e]) * c.max_pages + j;
+        drop_page(c, sh, freed, *at);
+        *at = -1;
+      });
+      if (tid < m) c.n_pages[sh.seq[tid]] = c.length[sh.seq[tid]] = 0;
+      __syncthreads();
+    }
     push_freed(c, sh, freed);
   }
   __syncthreads();
-  if (threadIdx.x == 0 && sh.bad) atomicOr(status, sh.bad);
+  if (tid == 0 && sh.bad) atomicOr(status, sh.bad);
 }
 
 // Workspace of fork and compact, after the 256-byte header.
@@ -270,85 +303,93 @@ __global__ void __launch_bounds__(CA_THREADS)
     cache_fork_kernel(ivc_cache c, const int32_t* src, const int32_t* dst, int n, int share,
                       ForkPlan plan, int* status) {
   __shared__ PlanShared sh;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_trigger();
-  plan_begin(c, sh);
-  const int fc = *c.free_count;
-  const int pt = c.page_tokens;
+  const int fc = plan_begin(c, sh);
+  const int tid = threadIdx.x, pt = c.page_tokens;
   auto copied = [&](int len) { return share ? (len % pt != 0) : (len + pt - 1) / pt; };
+  auto table_of = [&](int s) { return c.table + static_cast<size_t>(s) * c.max_pages; };
+  // pair base + tid into shared memory; later passes take the source's length as it
+  // stood before the call (an earlier pass may have made the source a target)
+  auto read = [&](int base, bool first_time) {
+    const int i = base + tid;
+    int bad = 0, need = 0;
+    if (i < n) {
+      const int s = src[i], d = dst[i];
+      int len = 0;
+      if (first_time) {
+        bad = claim_seq(c, sh, d);
+        if (!bad && (s < 0 || s >= c.max_seqs)) bad = DEV_BAD_CACHE;
+        if (!bad) bad = seq_sound(c, s);
+        if (!bad && (c.n_pages[d] != 0 || c.length[d] != 0)) bad = DEV_BAD_CACHE;
+        if (!bad) len = plan.len[i] = c.length[s];
+        if (bad) atomicOr(&sh.bad, bad);
+      } else {
+        len = plan.len[i];
+      }
+      need = bad ? 0 : copied(len);
+      sh.seq[tid] = d;
+      sh.from[tid] = s;
+      sh.len[tid] = len;
+    }
+    sh.need[tid] = need;
+    return need;
+  };
+  auto used = [&](int e) { return (sh.len[e] + pt - 1) / pt; };
   long long need = 0, total;
-  for (int i = threadIdx.x; i < n; i += CA_THREADS) {
-    const int s = src[i], d = dst[i];
-    int bad = claim_seq(c, sh, d);
-    if (!bad && (s < 0 || s >= c.max_seqs)) bad = DEV_BAD_CACHE;
-    if (!bad) bad = seq_sound(c, s);
-    if (!bad && (c.n_pages[d] != 0 || c.length[d] != 0)) bad = DEV_BAD_CACHE;
-    if (bad) {
-      atomicOr(&sh.bad, bad);
-      continue;
-    }
-    const int len = c.length[s];
-    plan.len[i] = len;
-    need += copied(len);
-  }
+  for (int base = 0; base < n; base += CA_THREADS) need += read(base, true);
   block_scan(need, sh.warp_sum, total);
-  if (threadIdx.x == 0 && total > fc) sh.bad |= DEV_CACHE_FULL;
-  __syncthreads();
-  bool go = sh.bad == 0;
-  __syncthreads();
+  if (tid == 0 && total > fc) sh.bad |= DEV_CACHE_FULL;
+  bool go = still_good(sh);
   if (go) {  // the pages that are read or shared have to be pages
-    for (int i = warp; i < n; i += CA_WARPS) {
-      const int32_t* row = c.table + static_cast<size_t>(src[i]) * c.max_pages;
-      for (int j = lane; j < (plan.len[i] + pt - 1) / pt; j += 32)
-        if (!page_ok(c, row[j]) || c.ref[row[j]] < 1) atomicOr(&sh.bad, DEV_BAD_CACHE);
+    for (int base = 0; base < n; base += CA_THREADS) {
+      if (n > CA_THREADS) {
+        __syncthreads();
+        read(base, false);
+        __syncthreads();
+      }
+      pages_of_pass(min(CA_THREADS, n - base), used, [&](int e, int j) {
+        const int p = table_of(sh.from[e])[j];
+        if (!page_ok(c, p) || c.ref[p] < 1) atomicOr(&sh.bad, DEV_BAD_CACHE);
+      });
     }
-    __syncthreads();
-    go = sh.bad == 0;
-    __syncthreads();
+    go = still_good(sh);
   }
   if (go) {
-    // the shared pages first: a new sequence's own pages come behind them
-    for (int i = warp; i < n; i += CA_WARPS) {
-      const int full = share ? plan.len[i] / pt : 0;
-      const int32_t* from = c.table + static_cast<size_t>(src[i]) * c.max_pages;
-      int32_t* to = c.table + static_cast<size_t>(dst[i]) * c.max_pages;
-      for (int j = lane; j < full; j += 32) {
-        to[j] = from[j];
-        atomicAdd(&c.ref[from[j]], 1);
-      }
-      if (lane == 0) {
-        c.n_pages[dst[i]] = full;
-        c.length[dst[i]] = plan.len[i];
-      }
-    }
-    __syncthreads();
     long long carry = 0;
     for (int base = 0; base < n; base += CA_THREADS) {
-      const int i = base + threadIdx.x;
-      const int mine = i < n ? copied(plan.len[i]) : 0;
+      if (n > CA_THREADS) {
+        __syncthreads();
+        read(base, false);
+      }
+      const int m = min(CA_THREADS, n - base);
       long long sum;
-      sh.order[threadIdx.x] = static_cast<int>(carry + block_scan(mine, sh.warp_sum, sum));
-      sh.need[threadIdx.x] = mine;
+      sh.order[tid] = static_cast<int>(carry + block_scan(sh.need[tid], sh.warp_sum, sum));
       __syncthreads();
-      take_pages(c, sh, dst, base, n, fc);
-      __syncthreads();
-      for (int e = warp; e < CA_THREADS && base + e < n; e += CA_WARPS) {
-        const int len = plan.len[base + e], k = sh.need[e];
-        const int first = (len + pt - 1) / pt - k;
-        const int32_t* from = c.table + static_cast<size_t>(src[base + e]) * c.max_pages + first;
-        const int32_t* to = c.table + static_cast<size_t>(dst[base + e]) * c.max_pages + first;
-        for (int j = lane; j < k; j += 32)
-          plan.jobs[sh.order[e] + j] =
-              make_int4(from[j], to[j], min(pt, len - (first + j) * pt), 0);
+      // the shared pages, and behind them new ones
+      pages_of_pass(m, used, [&](int e, int j) {
+        const int p = table_of(sh.from[e])[j], full = used(e) - sh.need[e];
+        int mine = p;
+        if (j < full) {
+          atomicAdd(&c.ref[p], 1);
+        } else {
+          const int k = sh.order[e] + j - full;
+          mine = take_page(c, sh, fc, k);
+          plan.jobs[k] = make_int4(p, mine, min(pt, sh.len[e] - j * pt), 0);
+        }
+        table_of(sh.seq[e])[j] = mine;
+      });
+      if (tid < m) {
+        c.n_pages[sh.seq[tid]] = used(tid);
+        c.length[sh.seq[tid]] = sh.len[tid];
       }
       carry += sum;
-      __syncthreads();
     }
-    if (threadIdx.x == 0) *c.free_count = fc - static_cast<int>(total);
+    __syncthreads();
+    if (tid == 0) *c.free_count = fc - static_cast<int>(total);
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
     *plan.n_jobs = go ? static_cast<int>(total) : 0;
     if (sh.bad) atomicOr(status, sh.bad);
   }
@@ -404,83 +445,95 @@ __global__ void __launch_bounds__(CA_THREADS)
                          int* status) {
   extern __shared__ unsigned freed[];
   __shared__ PlanShared sh;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_trigger();
   plan_begin(c, sh);
   clear_freed(c, freed);
-  const int pt = c.page_tokens;
-  auto first_of = [&](int i, int s) { return start ? start[i] : c.length[s]; };
-  for (int i = threadIdx.x; i < n; i += CA_THREADS) {
+  const int tid = threadIdx.x, pt = c.page_tokens;
+  // sequence base + tid: its first token, kept tokens and pages, into shared memory
+  auto read = [&](int base, bool first_time) {
+    const int i = base + tid;
+    if (i >= n) return;
     const int s = seq_of(seqs, i);
-    int bad = claim_seq(c, sh, s);
+    int bad = first_time ? claim_seq(c, sh, s) : 0;
     if (!bad) bad = seq_sound(c, s);
     if (!bad) {
-      const long long a = first_of(i, s), m = count[i];
-      if (a < 0 || a > c.length[s] || m < 0 || (keep && m > stride) ||
-          a + m > static_cast<long long>(c.n_pages[s]) * pt) {
+      const int len = c.length[s], np = c.n_pages[s];
+      const long long a = start ? start[i] : len, m = count[i];
+      if (a < 0 || a > len || m < 0 || (keep && m > stride) || a + m > static_cast<long long>(np) * pt) {
         bad = DEV_BAD_CACHE;
-      } else if ((a + m) % pt != 0) {  // the partly filled last page is nobody else's
+      } else if (first_time && (a + m) % pt != 0) {  // the partly filled last page is nobody else's
         const int p = c.table[static_cast<size_t>(s) * c.max_pages + (a + m) / pt];
         if (!page_ok(c, p) || c.ref[p] != 1) bad = DEV_BAD_CACHE;
       }
+      sh.seq[tid] = s;
+      sh.from[tid] = static_cast<int>(a);
+      sh.len[tid] = static_cast<int>(m);
+      sh.np[tid] = np;
     }
     if (bad) atomicOr(&sh.bad, bad);
-  }
-  __syncthreads();
-  bool go = sh.bad == 0;
-  __syncthreads();
+  };
+  for (int base = 0; base < n; base += CA_THREADS) read(base, true);
+  bool go = still_good(sh);
   if (go && keep) {
-    // every kept token on its own: rising, held, and its target a page of this
-    // sequence alone
-    const long long cells = static_cast<long long>(n) * stride;
-    for (long long e = threadIdx.x; e < cells; e += CA_THREADS) {
-      const int i = static_cast<int>(e / stride), j = static_cast<int>(e % stride);
-      if (j >= count[i]) continue;
-      const int s = seq_of(seqs, i);
-      const int32_t* row = c.table + static_cast<size_t>(s) * c.max_pages;
-      const long long a = first_of(i, s), k = keep[e];
-      const long long from = a + k, to = a + j;
-      const bool rises = k >= 0 && (j == 0 || keep[e - 1] < k);
-      if (!rises || from < to || from >= static_cast<long long>(c.n_pages[s]) * pt) {
-        atomicOr(&sh.bad, DEV_BAD_CACHE);
-        continue;
+    for (int base = 0; base < n; base += CA_THREADS) {
+      if (n > CA_THREADS) {
+        __syncthreads();
+        read(base, false);
+        __syncthreads();
       }
-      const int pf = row[from / pt], pd = row[to / pt];
-      if (!page_ok(c, pf) || !page_ok(c, pd) || (from != to && c.ref[pd] != 1)) {
-        atomicOr(&sh.bad, DEV_BAD_CACHE);
-        continue;
+      // every kept token on its own: rising, held, and its target a page of this
+      // sequence alone
+      const long long cells = static_cast<long long>(min(CA_THREADS, n - base)) * stride;
+      for (long long cell = tid; cell < cells; cell += CA_THREADS) {
+        const int e = static_cast<int>(cell / stride), j = static_cast<int>(cell - static_cast<long long>(e) * stride);
+        if (j >= sh.len[e]) continue;
+        const size_t at = static_cast<size_t>(base) * stride + cell;
+        const int32_t* row = c.table + static_cast<size_t>(sh.seq[e]) * c.max_pages;
+        const long long a = sh.from[e], k = keep[at];
+        const long long from = a + k, to = a + j;
+        const bool rises = k >= 0 && (j == 0 || keep[at - 1] < k);
+        if (!rises || from < to || from >= static_cast<long long>(sh.np[e]) * pt) {
+          atomicOr(&sh.bad, DEV_BAD_CACHE);
+          continue;
+        }
+        const int pf = row[from / pt], pd = row[to / pt];
+        if (!page_ok(c, pf) || !page_ok(c, pd) || (from != to && c.ref[pd] != 1)) {
+          atomicOr(&sh.bad, DEV_BAD_CACHE);
+          continue;
+        }
+        plan.rows[at] = make_int2(pf * pt + static_cast<int>(from % pt),
+                                  pd * pt + static_cast<int>(to % pt));
       }
-      plan.rows[e] = make_int2(pf * pt + static_cast<int>(from % pt),
-                               pd * pt + static_cast<int>(to % pt));
     }
-    __syncthreads();
-    go = sh.bad == 0;
-    __syncthreads();
+    go = still_good(sh);
   }
   if (keep)
-    for (int i = threadIdx.x; i < n; i += CA_THREADS) plan.count[i] = go ? count[i] : 0;
+    for (int i = tid; i < n; i += CA_THREADS) plan.count[i] = go ? count[i] : 0;
   if (go) {
-    for (int i = warp; i < n; i += CA_WARPS) {
-      const int s = seq_of(seqs, i);
-      const int len = first_of(i, s) + count[i];
-      const int np = c.n_pages[s], left = (len + pt - 1) / pt;
-      int32_t* row = c.table + static_cast<size_t>(s) * c.max_pages;
-      for (int j = left + lane; j < np; j += 32) {
-        drop_page(c, sh, freed, row[j]);
-        row[j] = -1;
+    for (int base = 0; base < n; base += CA_THREADS) {
+      if (n > CA_THREADS) {
+        __syncthreads();
+        read(base, false);
+        __syncthreads();
       }
-      __syncwarp();
-      if (lane == 0) {
-        c.length[s] = len;
-        c.n_pages[s] = min(np, left);
+      const int m = min(CA_THREADS, n - base);
+      auto left = [&](int e) { return (sh.from[e] + sh.len[e] + pt - 1) / pt; };
+      pages_of_pass(m, [&](int e) { return max(0, sh.np[e] - left(e)); }, [&](int e, int j) {
+        int32_t* at = c.table + static_cast<size_t>(sh.seq[e]) * c.max_pages + left(e) + j;
+        drop_page(c, sh, freed, *at);
+        *at = -1;
+      });
+      if (tid < m) {
+        c.length[sh.seq[tid]] = sh.from[tid] + sh.len[tid];
+        c.n_pages[sh.seq[tid]] = min(sh.np[tid], left(tid));
       }
     }
     __syncthreads();
     push_freed(c, sh, freed);
   }
   __syncthreads();
-  if (threadIdx.x == 0 && sh.bad) atomicOr(status, sh.bad);
+  if (tid == 0 && sh.bad) atomicOr(status, sh.bad);
 }
 
 // Moves the kept tokens of one sequence, plane (layer, keys or values) and
