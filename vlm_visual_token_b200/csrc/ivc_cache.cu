@@ -37,6 +37,7 @@ struct PlanShared {
   int order[CA_THREADS];            // pages taken before this sequence's
   int need[CA_THREADS];             // pages it takes
   long long warp_sum[CA_WARPS];
+  int widest;                       // compact: the most tokens kept of one sequence
   int bad;                          // DEV_* bits
 };
 
@@ -484,11 +485,18 @@ __global__ void __launch_bounds__(CA_THREADS)
       }
       // every kept token on its own: rising, held, and its target a page of this
       // sequence alone
-      const long long cells = static_cast<long long>(min(CA_THREADS, n - base)) * stride;
+      const int m = min(CA_THREADS, n - base);
+      if (tid == 0) sh.widest = 0;
+      __syncthreads();
+      if (tid < m) atomicMax(&sh.widest, sh.len[tid]);
+      __syncthreads();
+      const int width = sh.widest;
+      const long long cells = static_cast<long long>(m) * width;
       for (long long cell = tid; cell < cells; cell += CA_THREADS) {
-        const int e = static_cast<int>(cell / stride), j = static_cast<int>(cell - static_cast<long long>(e) * stride);
+        const int e = static_cast<int>(cell / width);
+        const int j = static_cast<int>(cell - static_cast<long long>(e) * width);
         if (j >= sh.len[e]) continue;
-        const size_t at = static_cast<size_t>(base) * stride + cell;
+        const size_t at = static_cast<size_t>(base + e) * stride + j;
         const int32_t* row = c.table + static_cast<size_t>(sh.seq[e]) * c.max_pages;
         const long long a = sh.from[e], k = keep[at];
         const long long from = a + k, to = a + j;
