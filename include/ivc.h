@@ -421,9 +421,9 @@ int ivc_cache_free(const ivc_cache* c, const int32_t* seqs, int n, void* workspa
  *   offsets    device int32 [B+1], 0 = o0 <= o1 <= ... <= oB <= N. Rows from
  *              oB on (a padded batch) are left as they were.
  *   q_out      device bf16 [N, q_heads, head_dim].
- * A token behind the pages that the sequence holds is not stored
- * (IVC_DEV_BAD_CACHE); bad offsets set IVC_DEV_BAD_TREE. q_heads a multiple of
- * kv_heads. */
+ * A sequence may be named once (two rows would store to one place). A token
+ * behind the pages that the sequence holds is not stored (IVC_DEV_BAD_CACHE);
+ * bad offsets set IVC_DEV_BAD_TREE. q_heads a multiple of kv_heads. */
 int ivc_qk_norm_rope(const ivc_cache* c, int layer, const void* qkv, long long ld, int N,
                      int q_heads, const void* q_gamma, const void* k_gamma, float eps, double theta,
                      const int32_t* positions, const int32_t* offsets, const int32_t* seqs, int B,

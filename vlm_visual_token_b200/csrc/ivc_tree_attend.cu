@@ -415,6 +415,7 @@ __device__ void mend_values(uint8_t* v, int base, int len, int n, int page_token
       }
   }
   if (found) *odd = 1;
+  __threadfence_block();  // the flag is read behind a barrier that a tcgen05.commit completes
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
 }
@@ -669,6 +670,7 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
         if (ok && mine_now && done == 0) {
           ok = warp_wait(&ofree, (items & 1) ^ 1);
           if (lane == 0) s_odd[items & 1][g] = 0;  // no epilogue reads it any more
+          __threadfence_block();
         }
         if (!ok) break;
         const int tile = it.t0 + t;
