@@ -1,0 +1,131 @@
+"""The decode step at the sizes its kernels are laid out for: attention with many key
+tiles per CTA and a maximum that keeps rising.
+
+Attention tolerance: weights and output rounded to bf16 (2^-8 relative each). A score is
+a sum of at most 128 fp32 products; with |q||k| scale below 2^9 it is off by less than
+2^9 * 2^-24 * 16 = 2^-11, its exponent (a product with scale * log2 e, rounded) by as
+much again, so that weights and their sum are off by 2^-10 relative each: 2^-9 of the
+weighted mean of |v|.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import decode_oracle as D
+from tests.test_gpu_decode import BF, _ivc, _tree, dev
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ attention
+def _long_case(lens, counts, Hq, kv, D_, pt, seed, rise):
+    """A cache whose keys grow along each context, so that a row's maximum rises by
+    2^8 and more again and again; the tokens of a page shuffled over the cache."""
+    ivc = _ivc()
+    B, N = len(lens), sum(counts)
+    need = [-(-(a + n) // pt) for a, n in zip(lens, counts)]
+    c = ivc.Cache.empty(1, sum(need) + 3, kv, pt, D_, B, max(need) + 1)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    c.free_list.copy_(torch.randperm(c.pages, generator=g, device="cuda"))
+    for name in ("k", "v"):
+        getattr(c, name).copy_(torch.randn(c.k.shape, generator=g, device="cuda"))
+    ivc.cache_reserve(c, dev(lens))
+    ivc.cache_compact(c, dev(lens))
+    ivc.cache_reserve(c, dev(counts))
+    for b in range(B):
+        pages = c.table[b, :need[b]].long()
+        t = torch.arange(need[b] * pt, device="cuda") / (lens[b] + counts[b])
+        grow = 0.05 * 2.0 ** (9 * t.clamp_max(1.0)) if rise else torch.ones_like(t)
+        c.k[0, pages] = (c.k[0, pages].float() * grow.view(-1, 1, pt, 1)).bfloat16()
+    q = torch.randn(N, Hq, D_, generator=g, device="cuda").bfloat16()
+    rng = np.random.RandomState(seed)
+    trees = [_tree(rng, n, "tree") for n in counts]
+    off = dev(np.concatenate([[0], np.cumsum(counts)]))
+    ws = ivc.new_workspace(ivc.tree_attention_workspace_size(c, N, Hq, B))
+    return ivc, c, q, trees, off, need, ws
+
+
+def _sees(tree, m):
+    n = len(tree)
+    see = torch.zeros(n, m + n, dtype=torch.bool)
+    see[:, :m] = True
+    for i in range(n):
+        see[i, [m + a for a in D.ancestors(tree, i)]] = True
+    return see.cuda()
+
+
+def _check_long(c, got, q, trees, lens, counts, need, Hq, kv, D_):
+    row = 0
+    for b, (m, n) in enumerate(zip(lens, counts)):
+        see = _sees(trees[b], m)
+        k, v = (x[0, c.table[b, :need[b]].long()].transpose(1, 2).reshape(-1, kv, D_)[:m + n].double()
+                for x in (c.k, c.v))
+        G = Hq // kv
+        for h in range(kv):
+            s = torch.einsum("ngd,ld->gnl", q[row:row + n, h * G:(h + 1) * G].double(), k[:, h]) * D_ ** -0.5
+            w = torch.softmax(s.masked_fill(~see, float("-inf")), -1)
+            want = torch.einsum("gnl,ld->ngd", w, v[:, h])
+            size = torch.einsum("gnl,ld->ngd", w, v[:, h].abs())
+            err = (got[row:row + n, h * G:(h + 1) * G].double() - want).abs()
+            assert bool((err <= BF * want.abs() + (BF + 2.0 ** -9) * size).all()), \
+                (b, h, float((err / size).max()))
+        row += n
+
+
+@pytest.mark.parametrize("lens,counts,Hq,kv,D_,pt", [
+    ([6100, 6000, 5900, 6333], [1] * 4, 32, 8, 128, 64),              # plain decoding
+    ([6100, 6000, 5900, 6333], [27, 1, 32, 9], 32, 8, 128, 16),       # up to 128 rows
+    ([6100, 6000, 5900, 6333], [64, 50, 33, 40], 32, 8, 128, 128),    # more than 128 rows
+    ([6100, 6000, 5901, 6333], [128, 100, 128, 77], 16, 8, 64, 32),   # drafted nodes over three tiles
+    ([6100, 6000, 5901], [128, 127, 90], 40, 8, 128, 64),             # 25 nodes of 5 heads a block
+    ([1200 + 17 * i for i in range(40)], [1 + i % 5 for i in range(40)], 8, 4, 64, 64),
+    ([2000 + 31 * i for i in range(36)], [33 + i % 40 for i in range(36)], 8, 2, 128, 64),
+])
+@pytest.mark.parametrize("rise", [True, False])
+def test_attention_with_many_tiles_per_cta(lens, counts, Hq, kv, D_, pt, rise):
+    tiles = sum(-(-(a + n) // 64) for a, n in zip(lens, counts)) * kv
+    assert tiles >= 8 * 148
+    ivc, c, q, trees, off, need, ws = _long_case(lens, counts, Hq, kv, D_, pt, 7, rise)
+    par = dev(sum(trees, []))
+    got = ivc.tree_attention(c, 0, q, par, off, workspace=ws)
+    assert ivc.device_status(ws) == 0
+    _check_long(c, got, q, trees, lens, counts, need, Hq, kv, D_)
+    for _ in range(3):                       # the order of the work does not matter
+        assert torch.equal(ivc.tree_attention(c, 0, q, par, off, workspace=ws), got)
+
+
+@pytest.mark.parametrize("Hq,kv,D_", [(40, 8, 128), (32, 8, 64), (6, 2, 128)])
+def test_a_row_does_not_depend_on_the_rows_beside_it(Hq, kv, D_):
+    """Every other node's queries replaced, by larger, smaller and non-finite ones: the
+    bits of the nodes between them stay, although they share the tiles' rows."""
+    lens, counts = [6100, 6000, 5901, 12000], [40, 27, 33, 5]
+    ivc, c, q, trees, off, need, ws = _long_case(lens, counts, Hq, kv, D_, 64, 3, True)
+    par = dev(sum(trees, []))
+    want = ivc.tree_attention(c, 0, q, par, off, workspace=ws)
+    for other in (20.0, 0.0, float("inf"), float("nan")):
+        changed = q.clone()
+        changed[::2] *= other
+        got = ivc.tree_attention(c, 0, changed, par, off, workspace=ws)
+        assert torch.equal(got[1::2], want[1::2]), other
+
+
+@pytest.mark.parametrize("Hq,counts", [(32, [64, 50, 33, 40]), (8, [64, 50, 33, 40]), (16, [128, 100, 128, 77])])
+def test_unseen_values_with_many_tiles_per_cta(Hq, counts):
+    """Every third node's value is not finite: only the rows that see it show it."""
+    lens, kv, D_ = [6100, 6000, 5901, 6333], 8, 64
+    ivc, c, q, trees, off, need, ws = _long_case(lens, counts, Hq, kv, D_, 32, 11, False)
+    trees = [[-1] + [0] * (n - 1) for n in counts]       # a star: a node is seen by itself alone
+    par = dev(sum(trees, []))
+    clean = ivc.tree_attention(c, 0, q, par, off, workspace=ws)
+    want = torch.zeros_like(clean, dtype=torch.bool)
+    bad, row = [float("nan"), float("inf"), -float("inf")], 0
+    for b, (m, n) in enumerate(zip(lens, counts)):
+        for i in range(2, n, 3):
+            page, slot = int(c.table[b, (m + i) // 32]), (m + i) % 32
+            c.v[0, page, :, slot, i % D_] = bad[i % 7 % 3]
+            want[row + i, :, i % D_] = True
+        row += n
+    got = ivc.tree_attention(c, 0, q, par, off, workspace=ws)
+    assert ivc.device_status(ws) == 0
+    assert torch.equal(~torch.isfinite(got.float()), want)
+    assert torch.equal(got[~want], clean[~want])

@@ -799,15 +799,17 @@ __global__ void __launch_bounds__(TA_THREADS, 1)
           const float rise = fmaxf(t0, t1) * a.scale_log2;
           if (u < 2) {
             m = rise;
-          } else if (__any_sync(0xffffffffu, rise - m > TA_RISE)) {
-            // once this group's sum before is complete (the one before that is:
-            // these scores lie in the columns of its weights)
+          } else if (const bool mine = r < rows && rise - m > TA_RISE; __any_sync(0xffffffffu, mine)) {
+            // a row is rescaled by its own scores alone (f is 1 for the others of the
+            // warp): its result does not depend on the rows beside it, nor on what
+            // shared memory held in those behind the block's last one. Once this
+            // group's sum before is complete (the one before that is: these scores lie
+            // in the columns of its weights)
             ok = warp_wait(&odone[g], (sums - 1) & 1);
             if (!ok) break;
             tc_fence_after();
-            const float m2 = fmaxf(m, rise);
-            const float f = m2 == -INFINITY ? 1.f : ex2(m - m2);
-            m = m2;
+            const float f = mine ? ex2(m - rise) : 1.f;
+            if (mine) m = rise;
             l *= f;
 #pragma unroll
             for (int d = 0; d < D; d += 32) {
