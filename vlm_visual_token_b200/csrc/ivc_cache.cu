@@ -7,11 +7,12 @@
 //
 // The plan is one CTA. It first checks everything that the operation is going
 // to touch, and only when all of it is sound changes the tables: a refused call
-// leaves the cache as it was. Counts are integers and pages are handed out by
-// prefix sums, so results do not depend on thread order; freed pages are
-// collected as bits of a bitmap in shared memory (one bit per page, at most
-// 128 KB), which both finds the last holder's release exactly once and lists
-// the freed pages in ascending order.
+// leaves the cache as it was. (Holders of pages to be given back are counted down
+// to see that there are enough of them, and up again where there are not.) Counts
+// are integers and pages are handed out by prefix sums, so results do not depend on
+// thread order; freed pages are collected as bits of a bitmap in shared memory (one
+// bit per page, at most 128 KB), which both finds the last holder's release exactly
+// once and lists the freed pages in ascending order.
 #include <cuda_runtime.h>
 
 #include "ivc_internal.h"
@@ -129,29 +130,23 @@ __device__ __forceinline__ int take_page(const ivc_cache& c, PlanShared& sh, int
   return -1;
 }
 
-// One holder less of page p; its bit is set when that was the last one.
+// One holder less of page p; its bit is set when that was the last one. A page that is
+// none or belongs to nobody makes the call bad, and give_back then takes all back.
 __device__ void drop_page(const ivc_cache& c, PlanShared& sh, unsigned* freed, int p) {
   if (!page_ok(c, p)) {
     atomicOr(&sh.bad, DEV_BAD_CACHE);
     return;
   }
   const int before = atomicSub(&c.ref[p], 1);
-  if (before == 1) {
-    atomicOr(&freed[p >> 5], 1u << (p & 31));
-  } else if (before < 1) {  // it belonged to nobody
-    atomicAdd(&c.ref[p], 1);
-    atomicOr(&sh.bad, DEV_BAD_CACHE);
-  }
+  if (before == 1) atomicOr(&freed[p >> 5], 1u << (p & 31));
+  else if (before < 1) atomicOr(&sh.bad, DEV_BAD_CACHE);
 }
 
-// Puts the pages of the bitmap on the free list, the lowest number on top.
-__device__ void push_freed(const ivc_cache& c, PlanShared& sh, const unsigned* freed) {
+// Puts the `total` pages of the bitmap behind the `fc` on the free list, the lowest
+// number on top; there is room for them.
+__device__ void push_freed(const ivc_cache& c, PlanShared& sh, const unsigned* freed, int fc,
+                           long long total) {
   const int words = (c.pages + 31) / 32;
-  long long mine = 0, total;
-  for (int i = threadIdx.x; i < words; i += CA_THREADS) mine += __popc(freed[i]);
-  block_scan(mine, sh.warp_sum, total);
-  if (total == 0) return;
-  const int fc = *c.free_count;
   long long carry = 0;
   for (int base = 0; base < words; base += CA_THREADS) {
     unsigned w = base + threadIdx.x < words ? freed[base + threadIdx.x] : 0u;
@@ -160,14 +155,35 @@ __device__ void push_freed(const ivc_cache& c, PlanShared& sh, const unsigned* f
     while (w) {
       const int b = __ffs(w) - 1;
       w &= w - 1;
-      const long long at = fc + total - 1 - rank++;
-      if (at < c.pages) c.free_list[at] = (base + threadIdx.x) * 32 + b;
-      else atomicOr(&sh.bad, DEV_BAD_CACHE);
+      c.free_list[fc + total - 1 - rank++] = (base + threadIdx.x) * 32 + b;
     }
     carry += sum;
   }
-  __syncthreads();
-  if (threadIdx.x == 0) *c.free_count = static_cast<int>(min(fc + total, (long long)c.pages));
+  if (threadIdx.x == 0) *c.free_count = fc + static_cast<int>(total);
+}
+
+// Gives back the pages that `each` names (it calls its argument with the address of
+// every table entry concerned, all threads together), if all of them are pages with a
+// holder and the list has room for those freed; else everything stays as it was. The
+// holders are counted first, which finds a wrong entry behind right ones and a page
+// named more often than it is held, and counted back where one was found.
+template <typename Each>
+__device__ bool give_back(const ivc_cache& c, PlanShared& sh, unsigned* freed, int fc, Each each) {
+  each([&](int32_t* at) { drop_page(c, sh, freed, *at); });
+  __syncthreads();  // the bitmap is complete
+  long long mine = 0, total;
+  for (int i = threadIdx.x; i < (c.pages + 31) / 32; i += CA_THREADS) mine += __popc(freed[i]);
+  block_scan(mine, sh.warp_sum, total);
+  if (threadIdx.x == 0 && fc + total > c.pages) sh.bad |= DEV_BAD_CACHE;
+  if (!still_good(sh)) {
+    each([&](int32_t* at) {
+      if (page_ok(c, *at)) atomicAdd(&c.ref[*at], 1);
+    });
+    return false;
+  }
+  each([&](int32_t* at) { *at = -1; });
+  if (total > 0) push_freed(c, sh, freed, fc, total);
+  return true;
 }
 
 __device__ void clear_freed(const ivc_cache& c, unsigned* freed) {
@@ -253,7 +269,7 @@ __global__ void __launch_bounds__(CA_THREADS)
   __shared__ PlanShared sh;
   pdl_wait();
   pdl_trigger();
-  plan_begin(c, sh);
+  const int fc = plan_begin(c, sh);
   clear_freed(c, freed);
   const int tid = threadIdx.x;
   auto read = [&](int base, bool first_time) {
@@ -269,22 +285,28 @@ __global__ void __launch_bounds__(CA_THREADS)
     sh.seq[tid] = s;
     sh.np[tid] = c.n_pages[s];
   };
-  for (int base = 0; base < n; base += CA_THREADS) read(base, true);
-  if (still_good(sh)) {
+  // f(pass) with the sequences of each pass in shared memory
+  auto passes = [&](auto f) {
     for (int base = 0; base < n; base += CA_THREADS) {
-      if (n > CA_THREADS) read(base, false);
-      __syncthreads();
-      const int m = min(CA_THREADS, n - base);
-      pages_of_pass(m, [&](int e) { return sh.np[e]; }, [&](int e, int j) {
-        int32_t* at = c.table + static_cast<size_t>(sh.seq[e]) * c.max_pages + j;
-        drop_page(c, sh, freed, *at);
-        *at = -1;
-      });
-      if (tid < m) c.n_pages[sh.seq[tid]] = c.length[sh.seq[tid]] = 0;
-      __syncthreads();
+      if (n > CA_THREADS) {
+        __syncthreads();
+        read(base, false);
+        __syncthreads();
+      }
+      f(min(CA_THREADS, n - base));
     }
-    push_freed(c, sh, freed);
-  }
+  };
+  for (int base = 0; base < n; base += CA_THREADS) read(base, true);
+  if (still_good(sh) && give_back(c, sh, freed, fc, [&](auto f) {
+        passes([&](int m) {
+          pages_of_pass(m, [&](int e) { return sh.np[e]; }, [&](int e, int j) {
+            f(c.table + static_cast<size_t>(sh.seq[e]) * c.max_pages + j);
+          });
+        });
+      }))
+    passes([&](int m) {
+      if (tid < m) c.n_pages[sh.seq[tid]] = c.length[sh.seq[tid]] = 0;
+    });
   __syncthreads();
   if (tid == 0 && sh.bad) atomicOr(status, sh.bad);
 }
@@ -448,7 +470,7 @@ __global__ void __launch_bounds__(CA_THREADS)
   __shared__ PlanShared sh;
   pdl_wait();
   pdl_trigger();
-  plan_begin(c, sh);
+  const int fc = plan_begin(c, sh);
   clear_freed(c, freed);
   const int tid = threadIdx.x, pt = c.page_tokens;
   // sequence base + tid: its first token, kept tokens and pages, into shared memory
@@ -516,30 +538,34 @@ __global__ void __launch_bounds__(CA_THREADS)
     }
     go = still_good(sh);
   }
-  if (keep)
-    for (int i = tid; i < n; i += CA_THREADS) plan.count[i] = go ? count[i] : 0;
-  if (go) {
+  auto left = [&](int e) { return (sh.from[e] + sh.len[e] + pt - 1) / pt; };
+  // f(pass) with the sequences of each pass in shared memory
+  auto passes = [&](auto f) {
     for (int base = 0; base < n; base += CA_THREADS) {
       if (n > CA_THREADS) {
         __syncthreads();
         read(base, false);
         __syncthreads();
       }
-      const int m = min(CA_THREADS, n - base);
-      auto left = [&](int e) { return (sh.from[e] + sh.len[e] + pt - 1) / pt; };
+      f(min(CA_THREADS, n - base));
+    }
+  };
+  go = go && give_back(c, sh, freed, fc, [&](auto f) {
+    passes([&](int m) {
       pages_of_pass(m, [&](int e) { return max(0, sh.np[e] - left(e)); }, [&](int e, int j) {
-        int32_t* at = c.table + static_cast<size_t>(sh.seq[e]) * c.max_pages + left(e) + j;
-        drop_page(c, sh, freed, *at);
-        *at = -1;
+        f(c.table + static_cast<size_t>(sh.seq[e]) * c.max_pages + left(e) + j);
       });
+    });
+  });
+  if (go)
+    passes([&](int m) {
       if (tid < m) {
         c.length[sh.seq[tid]] = sh.from[tid] + sh.len[tid];
         c.n_pages[sh.seq[tid]] = min(sh.np[tid], left(tid));
       }
-    }
-    __syncthreads();
-    push_freed(c, sh, freed);
-  }
+    });
+  if (keep)
+    for (int i = tid; i < n; i += CA_THREADS) plan.count[i] = go ? count[i] : 0;
   __syncthreads();
   if (tid == 0 && sh.bad) atomicOr(status, sh.bad);
 }
