@@ -72,6 +72,50 @@ def test_pages_that_cannot_be_given_back(what, change):
                                                 dev([0] * 4), dev(order), workspace=p.ws))
 
 
+def _entry(value):
+    def change(c):
+        c.free_list[int(c.free_count) - 2] = value
+    return change
+
+
+def _held(c):
+    _entry(int(c.table[0, 0]))(c)
+
+
+def _twice(c):
+    _entry(int(c.free_list[int(c.free_count) - 1]))(c)
+
+
+@pytest.mark.parametrize("change", [_entry(-1), _entry(64), _entry(1 << 30), _held, _twice])
+@pytest.mark.parametrize("what", ["reserve one", "reserve several", "fork", "fork shared"])
+def test_pages_that_cannot_be_taken(what, change):
+    """The second page from the top of the free list is none, held, or there twice."""
+    p = _batch()
+    change(p.gpu)
+    call = {"reserve one": lambda: p.ivc.cache_reserve(p.gpu, dev([48]), dev([5]), workspace=p.ws),
+            "reserve several": lambda: p.ivc.cache_reserve(p.gpu, dev([3, 10, 16]), dev([5, 6, 7]),
+                                                           workspace=p.ws),
+            "fork": lambda: p.ivc.cache_fork(p.gpu, dev([2]), dev([5]), False, workspace=p.ws),
+            "fork shared": lambda: p.ivc.cache_fork(p.gpu, dev([0, 1]), dev([6, 5]), True, workspace=p.ws)}
+    _refused(p, call[what])
+
+
+def test_a_wrong_entry_that_is_not_touched_does_not_matter():
+    """The third entry from the top: a call that takes two pages is right, the next is refused."""
+    p = _batch()
+    at = int(p.gpu.free_count) - 3
+    was = int(p.gpu.free_list[at])
+    p.gpu.free_list[at] = 1 << 30
+    p.ivc.cache_reserve(p.gpu, dev([20]), dev([5]), workspace=p.ws)
+    assert p.ivc.device_status(p.ws) == 0
+    _refused(p, lambda: p.ivc.cache_reserve(p.gpu, dev([20]), dev([6]), workspace=p.ws))
+    p.gpu.free_list[at] = was
+    p.ref.reserve([20], [5])
+    p.same()
+    p.reserve([20], [6])
+    p.free([5, 6, 0, 3])
+
+
 def test_a_wrong_entry_behind_many_sequences():
     """More sequences than a CTA has threads, the wrong page in the last ones."""
     n, pt = 1500, 16
@@ -79,7 +123,7 @@ def test_a_wrong_entry_behind_many_sequences():
     p.ws = p.ivc.new_workspace(p.ivc.cache_workspace_size(p.gpu, n, 0))
     lens = np.random.RandomState(0).randint(1, 3 * pt, n).tolist()
     lens[-1] = 3 * pt
-    seqs = list(range(n))
+    seqs, rest = list(range(n)), list(range(n, 2 * n))
     p.reserve(lens, seqs)
     p.compact(lens, seqs=seqs)
     good = int(p.gpu.table[n - 1, 2])
@@ -87,5 +131,11 @@ def test_a_wrong_entry_behind_many_sequences():
     _refused(p, lambda: p.ivc.cache_free(p.gpu, dev(seqs), workspace=p.ws))
     _refused(p, lambda: p.ivc.cache_compact(p.gpu, dev([0] * n), None, dev([0] * n), dev(seqs), workspace=p.ws))
     p.gpu.table[n - 1, 2] = good
+    at = int(p.gpu.free_count) - n
+    entry = int(p.gpu.free_list[at])
+    p.gpu.free_list[at] = good               # the n-th page taken is another's
+    _refused(p, lambda: p.ivc.cache_reserve(p.gpu, dev([1] * n), dev(rest), workspace=p.ws))
+    _refused(p, lambda: p.ivc.cache_fork(p.gpu, dev(seqs), dev(rest), False, workspace=p.ws))
+    p.gpu.free_list[at] = entry
     p.same()
     p.free(seqs)

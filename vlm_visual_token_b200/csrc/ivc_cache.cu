@@ -116,18 +116,31 @@ __device__ bool still_good(const PlanShared& sh) {
   return good;
 }
 
-// The k-th page that this call takes off the free list; -1 (and DEV_BAD_CACHE) where
-// the list holds no page there.
-__device__ __forceinline__ int take_page(const ivc_cache& c, PlanShared& sh, int free_count, int k) {
+// Clears the bitmap of pages; a barrier of the plan stands before its first use.
+__device__ void clear_pages(const ivc_cache& c, unsigned* pages) {
+  for (int i = threadIdx.x; i < (c.pages + 31) / 32; i += CA_THREADS) pages[i] = 0;
+}
+
+// The `total` pages on top of the free list are pages that nobody holds, each there
+// once (a bit per page in `taken`, which is clear). Without this a page listed twice or
+// still held would get two owners, and the next store would spoil another sequence.
+__device__ void check_top(const ivc_cache& c, PlanShared& sh, unsigned* taken, int free_count,
+                          int total) {
+  for (int k = threadIdx.x; k < total; k += CA_THREADS) {
+    const int p = c.free_list[free_count - 1 - k];
+    const unsigned bit = 1u << (p & 31);
+    if (!page_ok(c, p) || c.ref[p] != 0 || (atomicOr(&taken[p >> 5], bit) & bit))
+      atomicOr(&sh.bad, DEV_BAD_CACHE);
+  }
+}
+
+// The k-th page that this call takes off the free list.
+__device__ __forceinline__ int take_page(const ivc_cache& c, int free_count, int k) {
   const int at = free_count - 1 - k;
   const int p = c.free_list[at];
   c.free_list[at] = -1;
-  if (page_ok(c, p)) {
-    c.ref[p] = 1;
-    return p;
-  }
-  atomicOr(&sh.bad, DEV_BAD_CACHE);
-  return -1;
+  c.ref[p] = 1;
+  return p;
 }
 
 // One holder less of page p; its bit is set when that was the last one. A page that is
@@ -186,10 +199,6 @@ __device__ bool give_back(const ivc_cache& c, PlanShared& sh, unsigned* freed, i
   return true;
 }
 
-__device__ void clear_freed(const ivc_cache& c, unsigned* freed) {
-  for (int i = threadIdx.x; i < (c.pages + 31) / 32; i += CA_THREADS) freed[i] = 0;
-}
-
 __global__ void __launch_bounds__(256) cache_init_kernel(ivc_cache c) {
   pdl_wait();
   pdl_trigger();
@@ -208,10 +217,12 @@ __global__ void __launch_bounds__(256) cache_init_kernel(ivc_cache c) {
 __global__ void __launch_bounds__(CA_THREADS)
     cache_reserve_kernel(ivc_cache c, const int32_t* tokens, const int32_t* seqs, int n,
                          int* status) {
+  extern __shared__ unsigned taken[];
   __shared__ PlanShared sh;
   pdl_wait();
   pdl_trigger();
   const int fc = plan_begin(c, sh);
+  clear_pages(c, taken);
   const int tid = threadIdx.x;
   // sequence base + tid: its number, pages, and the pages it lacks for length +
   // tokens[] tokens, into shared memory
@@ -241,7 +252,12 @@ __global__ void __launch_bounds__(CA_THREADS)
   for (int base = 0; base < n; base += CA_THREADS) need += read(base, true);
   block_scan(need, sh.warp_sum, total);
   if (tid == 0 && total > fc) sh.bad |= DEV_CACHE_FULL;
-  if (still_good(sh) && total > 0) {
+  bool go = still_good(sh) && total > 0;
+  if (go) {
+    check_top(c, sh, taken, fc, static_cast<int>(total));
+    go = still_good(sh);
+  }
+  if (go) {
     long long carry = 0;
     for (int base = 0; base < n; base += CA_THREADS) {
       if (n > CA_THREADS) read(base, false);
@@ -251,7 +267,7 @@ __global__ void __launch_bounds__(CA_THREADS)
       __syncthreads();
       pages_of_pass(m, [&](int e) { return sh.need[e]; }, [&](int e, int j) {
         c.table[static_cast<size_t>(sh.seq[e]) * c.max_pages + sh.np[e] + j] =
-            take_page(c, sh, fc, sh.order[e] + j);
+            take_page(c, fc, sh.order[e] + j);
       });
       if (tid < m && sh.need[tid] > 0) c.n_pages[sh.seq[tid]] = sh.np[tid] + sh.need[tid];
       carry += sum;
@@ -270,7 +286,7 @@ __global__ void __launch_bounds__(CA_THREADS)
   pdl_wait();
   pdl_trigger();
   const int fc = plan_begin(c, sh);
-  clear_freed(c, freed);
+  clear_pages(c, freed);
   const int tid = threadIdx.x;
   auto read = [&](int base, bool first_time) {
     const int i = base + tid;
@@ -325,10 +341,12 @@ struct CompactPlan {
 __global__ void __launch_bounds__(CA_THREADS)
     cache_fork_kernel(ivc_cache c, const int32_t* src, const int32_t* dst, int n, int share,
                       ForkPlan plan, int* status) {
+  extern __shared__ unsigned taken[];
   __shared__ PlanShared sh;
   pdl_wait();
   pdl_trigger();
   const int fc = plan_begin(c, sh);
+  clear_pages(c, taken);
   const int tid = threadIdx.x, pt = c.page_tokens;
   auto copied = [&](int len) { return share ? (len % pt != 0) : (len + pt - 1) / pt; };
   auto table_of = [&](int s) { return c.table + static_cast<size_t>(s) * c.max_pages; };
@@ -364,7 +382,8 @@ __global__ void __launch_bounds__(CA_THREADS)
   block_scan(need, sh.warp_sum, total);
   if (tid == 0 && total > fc) sh.bad |= DEV_CACHE_FULL;
   bool go = still_good(sh);
-  if (go) {  // the pages that are read or shared have to be pages
+  if (go) {  // the pages that are taken, read or shared have to be pages
+    check_top(c, sh, taken, fc, static_cast<int>(total));
     for (int base = 0; base < n; base += CA_THREADS) {
       if (n > CA_THREADS) {
         __syncthreads();
@@ -397,7 +416,7 @@ __global__ void __launch_bounds__(CA_THREADS)
           atomicAdd(&c.ref[p], 1);
         } else {
           const int k = sh.order[e] + j - full;
-          mine = take_page(c, sh, fc, k);
+          mine = take_page(c, fc, k);
           plan.jobs[k] = make_int4(p, mine, min(pt, sh.len[e] - j * pt), 0);
         }
         table_of(sh.seq[e])[j] = mine;
@@ -471,7 +490,7 @@ __global__ void __launch_bounds__(CA_THREADS)
   pdl_wait();
   pdl_trigger();
   const int fc = plan_begin(c, sh);
-  clear_freed(c, freed);
+  clear_pages(c, freed);
   const int tid = threadIdx.x, pt = c.page_tokens;
   // sequence base + tid: its first token, kept tokens and pages, into shared memory
   auto read = [&](int base, bool first_time) {
@@ -712,8 +731,10 @@ int ivc_cache_reserve(const ivc_cache* c, const int32_t* tokens, const int32_t* 
   if (const int rc = step_ws_ok(workspace, ws_bytes, IVC_STEP_WORKSPACE_BYTES)) return rc;
   if (n == 0) return IVC_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const size_t smem = bitmap_bytes(c);
+  if (const int rc = smem_optin(reinterpret_cast<const void*>(cache_reserve_kernel), smem)) return rc;
   TraceScope ts("cache.reserve", s);
-  return launch_k(cache_reserve_kernel, dim3(1), dim3(CA_THREADS), 0, s, 1, *c, tokens, seqs, n,
+  return launch_k(cache_reserve_kernel, dim3(1), dim3(CA_THREADS), smem, s, 1, *c, tokens, seqs, n,
                   static_cast<int*>(workspace));
 }
 
@@ -743,9 +764,11 @@ int ivc_cache_fork(const ivc_cache* c, const int32_t* src, const int32_t* dst, i
   plan.n_jobs = reinterpret_cast<int32_t*>(w);
   plan.len = reinterpret_cast<int32_t*>(w + 256);
   plan.jobs = reinterpret_cast<int4*>(w + 256 + up256(static_cast<size_t>(n) * 4));
+  const size_t smem = bitmap_bytes(c);
+  if (const int rc = smem_optin(reinterpret_cast<const void*>(cache_fork_kernel), smem)) return rc;
   {
     TraceScope ts("cache.fork", s);
-    const int rc = launch_k(cache_fork_kernel, dim3(1), dim3(CA_THREADS), 0, s, 1, *c, src, dst, n,
+    const int rc = launch_k(cache_fork_kernel, dim3(1), dim3(CA_THREADS), smem, s, 1, *c, src, dst, n,
                             share, plan, static_cast<int*>(workspace));
     if (rc != IVC_OK) return rc;
   }
