@@ -264,8 +264,8 @@ def cache_free(cache: Cache, seqs: torch.Tensor, workspace=None, stream=None) ->
 
 
 def _out(out, N: int, q_heads: int, D: int, device):
-    if out is None:
-        return torch.empty(N, q_heads, D, dtype=torch.bfloat16, device=device)
+    if out is None:  # zeros: rows of skipped sequences and behind the last one are not written
+        return torch.zeros(N, q_heads, D, dtype=torch.bfloat16, device=device)
     _need(out, "out", torch.bfloat16, 3, device)
     if out.shape != (N, q_heads, D):
         _refuse("out: [N, q_heads, head_dim] is needed")
@@ -278,7 +278,8 @@ def qk_norm_rope(cache: Cache, layer: int, qkv: torch.Tensor, q_gamma: torch.Ten
                  out: Optional[torch.Tensor] = None, workspace=None, stream=None) -> torch.Tensor:
     """Per-head norms and rotation of the packed projections qkv [N, (q_heads + 2
     kv_heads) * head_dim] (rows may be strided); keys and values go to the cache
-    behind the committed tokens, the queries [N, q_heads, head_dim] are returned."""
+    behind the committed tokens, the queries [N, q_heads, head_dim] are returned
+    (in `out`; without it, rows behind the last sequence are zero)."""
     dev, D = cache.device, cache.head_dim
     other = _elsewhere(dev, stream)
     if other is not None:
@@ -320,7 +321,9 @@ def tree_attention(cache: Cache, layer: int, q: torch.Tensor, parents: Optional[
                    workspace=None, stream=None) -> torch.Tensor:
     """Attention of the trees' nodes q [N, q_heads, head_dim] (tokens may be
     strided) over their committed tokens, ancestors and themselves. parents None:
-    chains. scale: 1 / sqrt(head_dim) by default."""
+    chains. scale: 1 / sqrt(head_dim) by default. Rows of sequences that are skipped
+    (device_status tells) and behind the last one stay as they are in `out`;
+    without `out` they are zero."""
     dev, D = cache.device, cache.head_dim
     other = _elsewhere(dev, stream)
     if other is not None:
