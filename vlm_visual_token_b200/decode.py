@@ -2,17 +2,22 @@
 decode step (include/ivc.h, "Decoding behind the spliced sequence").
 
     cache = Cache.empty(layers, pages, kv_heads, page_tokens, head_dim, max_seqs, max_pages)
-    cache_reserve(cache, tokens)                  # pages for the new tokens
-    q = qk_norm_rope(cache, layer, qkv, q_gamma, k_gamma, positions, offsets)
-    out = tree_attention(cache, layer, q, parents, offsets)
-    path, n_path, token = verify_drafts(p, draft_p, tokens, parents, offsets, u, u_next)
-    cache_compact(cache, n_path, path)            # the accepted tokens stay, the rest is freed
+    ws = new_workspace(max(tree_attention_workspace_size(cache, N, q_heads, B),
+                           cache_workspace_size(cache, B, MAX_TREE)))
+    cache_reserve(cache, tokens, workspace=ws)    # pages for the new tokens
+    q = qk_norm_rope(cache, layer, qkv, q_gamma, k_gamma, positions, offsets, workspace=ws)
+    out = tree_attention(cache, layer, q, parents, offsets, workspace=ws)
+    path, n_path, token = verify_drafts(p, draft_p, tokens, parents, offsets, u, u_next, workspace=ws)
+    cache_compact(cache, n_path, path, workspace=ws)  # the accepted tokens stay, the rest is freed
+    bits = device_status(ws)                      # 0, or what went wrong since the last look
 
 Argument marshalling only, as in the rest of the package. A call runs on
 `stream` (default: the current stream of the cache's device), its outputs and
 an omitted workspace are made on that stream. A wrong argument raises IvcError
-before anything is enqueued; wrong device data set bits of the workspace's
-status word (device_status).
+before anything is enqueued. Wrong device data, and a cache without enough free
+pages, set bits of the workspace's status word (device_status) and nothing else
+tells of them: a call without a workspace drops its bits. Outputs that a call
+makes itself are zero where it writes nothing.
 """
 from __future__ import annotations
 
