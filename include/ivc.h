@@ -444,7 +444,10 @@ int ivc_qk_norm_rope(const ivc_cache* c, int layer, const void* qkv, long long l
  * Scores, statistics and sums in fp32; the weights are rounded to bf16 for
  * their product with v. scale > 0; q_heads / kv_heads <= 64; B <= 4096. A tree with bad
  * offsets is skipped, a bad parent counts as -1 (IVC_DEV_BAD_TREE); a sequence
- * whose tokens are not all in its pages is skipped (IVC_DEV_BAD_CACHE). */
+ * whose tokens are not all in its pages is skipped (IVC_DEV_BAD_CACHE). The rows
+ * of what is skipped are left as they were. A prompt of more than IVC_MAX_TREE
+ * tokens goes through the layers in pieces of at most so many (parents NULL), each
+ * reserved, stored, attended and committed (ivc_cache_compact) before the next. */
 size_t ivc_tree_attention_workspace_size(const ivc_cache* c, int N, int q_heads, int B);
 int ivc_tree_attention(const ivc_cache* c, int layer, const void* q, long long q_ld, int N,
                        int q_heads, float scale, const int32_t* parents, const int32_t* offsets,
