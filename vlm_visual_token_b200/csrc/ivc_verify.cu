@@ -71,6 +71,14 @@ __device__ __forceinline__ double above_zero(double x) {
   return __hiloint2double(hi & keep, __double2loint(x) & keep);
 }
 
+// r / z - q / w as the formula has it: both products rounded. Fused, one of them would
+// not be, and where the two are equal (all that is left of the draft is left of the
+// target, and a sibling repeats a rejected token) the remainder would be 1e-17 of
+// noise instead of 0: more siblings tried, and the next token drawn from the noise.
+__device__ __forceinline__ double less(double r, double iz, double q, double iw) {
+  return __dsub_rn(__dmul_rn(r, iz), __dmul_rn(q, iw));
+}
+
 // VF_BATCH tokens v0, v0 + step, ... below `end`: their inputs (0 for the others) ...
 struct Batch {
   float p[VF_BATCH], q[VF_BATCH];
@@ -100,7 +108,7 @@ __device__ __forceinline__ void left_of(const Batch& x, bool dense, int v0, int 
     for (int i = 1; i < n; ++i) {
       const double iz = rj.iz[i], iw = rj.iw[i];
 #pragma unroll
-      for (int e = 0; e < VF_BATCH; ++e) r[e] = above_zero(r[e] * iz - d[e] * iw);
+      for (int e = 0; e < VF_BATCH; ++e) r[e] = above_zero(less(r[e], iz, d[e], iw));
     }
     return;
   }
@@ -239,7 +247,7 @@ __global__ void __launch_bounds__(VF_THREADS, 2)
     double r = positive(s_p[j]), d = q != nullptr ? positive(s_q[j]) : 1.0;
     for (int i = 0; i < rj.n; ++i) {
       if (q != nullptr) {
-        r = r * rj.iz[i] - d * rj.iw[i];
+        r = less(r, rj.iz[i], d, rj.iw[i]);
         r = r > 0.0 ? r : 0.0;
       }
       if (rj.token[i] == tok) {
