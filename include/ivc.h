@@ -442,7 +442,7 @@ int ivc_qk_norm_rope(const ivc_cache* c, int layer, const void* qkv, long long l
  *   out    device bf16 [N, q_heads, head_dim]; rows from offsets[B] on are left
  *          as they were.
  * Scores, statistics and sums in fp32; the weights are rounded to bf16 for
- * their product with v. scale > 0; q_heads / kv_heads <= 64; B <= 4096. A tree with bad
+ * their product with v. 0 < scale < 2e38; q_heads / kv_heads <= 64; B <= 4096. A tree with bad
  * offsets is skipped, a bad parent counts as -1 (IVC_DEV_BAD_TREE); a sequence
  * whose tokens are not all in its pages is skipped (IVC_DEV_BAD_CACHE). The rows
  * of what is skipped are left as they were. A prompt of more than IVC_MAX_TREE

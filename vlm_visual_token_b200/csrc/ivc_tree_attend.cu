@@ -1094,7 +1094,8 @@ int ivc_tree_attention(const ivc_cache* c, int layer, const void* q, long long q
                        ivc_stream_t stream) {
   if (const int rc = cache_ok(c)) return rc;
   if (layer < 0 || layer >= c->layers || N < 0 || B < 0 || q_heads < 1) return IVC_EINVAL;
-  if (!(scale > 0.f && scale < INFINITY)) return IVC_EINVAL;
+  const float scale_log2 = scale * 1.4426950408889634f;  // infinite times a score of 0 is NaN
+  if (!(scale > 0.f && scale_log2 < INFINITY)) return IVC_EINVAL;
   if (q_heads % c->kv_heads != 0 || q_heads / c->kv_heads > 64 || B > TA_MAX_BATCH)
     return IVC_EUNSUPPORTED;
   if (q_ld % 8 != 0 || q_ld < static_cast<long long>(q_heads) * c->head_dim) return IVC_EUNSUPPORTED;
@@ -1113,7 +1114,7 @@ int ivc_tree_attention(const ivc_cache* c, int layer, const void* q, long long q
   a.npt = TA_ROWS / a.group;
   a.layer = layer;
   a.B = B;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.parents = parents;
   a.offsets = offsets;
   a.seqs = seqs;
