@@ -1,5 +1,6 @@
 """The decode step at the sizes its kernels are laid out for: attention with many key
-tiles per CTA and a maximum that keeps rising.
+tiles per CTA and a maximum that keeps rising, verification over vocabularies that a
+cluster of CTAs shares, compactions in which a CTA moves several heads.
 
 Attention tolerance: weights and output rounded to bf16 (2^-8 relative each). A score is
 a sum of at most 128 fp32 products; with |q||k| scale below 2^9 it is off by less than
@@ -12,7 +13,7 @@ import pytest
 import torch
 
 from oracle import decode_oracle as D
-from tests.test_gpu_decode import BF, _ivc, _tree, dev
+from tests.test_gpu_decode import BF, Pair, _ivc, _tree, _verify_case, _verify_check, dev
 
 pytestmark = pytest.mark.gpu
 
@@ -129,3 +130,115 @@ def test_unseen_values_with_many_tiles_per_cta(Hq, counts):
     assert ivc.device_status(ws) == 0
     assert torch.equal(~torch.isfinite(got.float()), want)
     assert torch.equal(got[~want], clean[~want])
+
+
+# ------------------------------------------------------------------ verification
+@pytest.mark.parametrize("dense", [False, True])
+@pytest.mark.parametrize("V", [4096, 4097, 32000, 151001, 300001])
+def test_verification_over_large_vocabularies(V, dense):
+    """Rejections and draws at the ends and in the middle of the random numbers' range."""
+    rng = np.random.RandomState(V % 1000 + dense)
+    counts = [1, 6, 5, 0, 7, 2, 4]
+    p, q, tok, trees, off, u, un = _verify_case(rng, counts, V, dense, "tree")
+    top = float(np.nextafter(np.float32(1), np.float32(0)))
+    for us, draws in ((u, un), (np.full_like(u, top), np.full_like(un, 0.5)),
+                      (np.full_like(u, top), np.full_like(un, top)), (0.5 + u / 2, np.zeros_like(un)),
+                      (np.zeros_like(u), np.full_like(un, 1e-7))):
+        _verify_check(_ivc(), p, q, tok, trees, off, us, draws)
+
+
+@pytest.mark.parametrize("dense", [False, True])
+def test_verification_of_wide_trees_and_strided_rows_over_a_large_vocabulary(dense):
+    rng = np.random.RandomState(13)
+    case = _verify_case(rng, [128, 100], 5003, dense, "tree", peaked=0.3)
+    _verify_check(_ivc(), *case, width=128, ld=5010)
+    star = _verify_case(rng, [128, 3], 4999, dense, "star", peaked=0.1)
+    _verify_check(_ivc(), *star, width=128)
+    *most, u, un = star
+    _verify_check(_ivc(), *most, np.nextafter(np.ones_like(u), np.float32(0)), un, width=128)
+
+
+@pytest.mark.parametrize("at", [[0, 1, 2, 3], [4999, 0, 625, 624], [10, 2600, 4374, 4375]])
+def test_verification_borders_over_a_large_vocabulary(at):
+    """Certain tokens, equal distributions and rows that leave nothing, wherever the few
+    tokens that have a probability stand in the CTAs' slices."""
+    ivc, V = _ivc(), 5000
+    chain, off = [[-1, 0, 1]], np.array([0, 3], np.int32)
+    u0, un = np.zeros(3, np.float32), np.array([0.0], np.float32)
+    top = np.full(3, np.nextafter(np.float32(1), np.float32(0)), np.float32)
+    t = lambda *x: np.array([0] + [at[i] for i in x], np.int32)  # noqa: E731
+
+    def rows(x):
+        big = np.zeros((len(x), V), np.float32)
+        big[:, at] = x
+        return big
+
+    one = rows(np.eye(4, dtype=np.float32))
+    _verify_check(ivc, one[[1, 2, 3]], None, t(1, 2), chain, off, top, un)
+    _verify_check(ivc, one[[2, 2, 3]], None, t(1, 2), chain, off, u0, un)
+    flat = rows(np.array([[0.5, 0.5, 0, 0]] * 3))
+    _verify_check(ivc, flat, flat, t(1, 0), chain, off, top, un)
+    _verify_check(ivc, flat, flat, t(2, 0), chain, off, u0, un)
+    _verify_check(ivc, flat, None, t(2, 3), [[-1, 0, 0]], off, u0, un)
+    for last in (0.0, 0.49999997, 0.5, float(top[0])):
+        _verify_check(ivc, flat[:1], None, t(), [[-1]], off[:1].tolist() + [1], u0[:1],
+                      np.array([last], np.float32))
+    four = rows(np.array([[0.1, 0.2, 0.3, 0.4]] * 4))
+    back = rows(np.array([[0.4, 0.3, 0.2, 0.1]] * 4))
+    for q in (None, back):
+        _verify_check(ivc, four, q, t(1, 1, 1), [[-1, 0, 0, 0]], np.array([0, 4], np.int32),
+                      np.full(4, 0.9, np.float32), np.array([0.6], np.float32))
+
+
+def test_verification_of_bad_rows_over_a_large_vocabulary():
+    ivc, V = _ivc(), 5000
+    rng = np.random.RandomState(2)
+    p, q, tok, trees, off, u, un = _verify_case(rng, [3, 3], V, True, "chain")
+    f = lambda x: dev(x, torch.float32)  # noqa: E731
+    ws = ivc.new_workspace(256)
+
+    def run(p=p, tok=tok, off=off):
+        r = ivc.verify_drafts(f(p), f(q), dev(tok), None, dev(off), f(u), f(un), path_width=4, workspace=ws)
+        return [x.cpu() for x in r], ivc.device_status(ws)
+
+    good, st = run()
+    assert st == 0
+    zero = p.copy()
+    zero[3:] = 0
+    (path, m, t), st = run(p=zero)
+    assert st == 256 and int(t[1]) == -1 and int(m[1]) == 1 and int(t[0]) == int(good[2][0])
+    for x in (np.nan, -1.0):
+        odd = p.copy()
+        odd[:3] = x
+        odd[:3, 4990] = 0.25
+        (path, m, t), st = run(p=odd)
+        assert st == 0 and int(t[0]) == 4990
+    odd = p.copy()
+    odd[:3, 2600] = np.inf
+    (path, m, t), st = run(p=odd, tok=np.zeros_like(tok))
+    assert st == 256 and int(t[0]) == -1
+    wrong = tok.copy()
+    wrong[1], wrong[4] = V, -3
+    (path, m, t), st = run(tok=wrong)
+    assert st == 256 and m.tolist() == [1, 1] and (t >= 0).all()
+    (path, m, t), st = run(off=np.array([0, 5, 3], np.int32))
+    assert st & 128 and int(m[1]) == 0 and int(t[1]) == -1
+
+
+# ------------------------------------------------------------------ compaction
+@pytest.mark.parametrize("kv,layers,n,D_", [(5, 12, 48, 64), (8, 10, 64, 64), (7, 6, 60, 128)])
+def test_compaction_with_several_heads_per_cta(kv, layers, n, D_):
+    """Many sequences and layers: a CTA moves a group of heads (the last group smaller,
+    or all heads), over more than one chunk of rows."""
+    ivc, pt = _ivc(), 16
+    p = Pair(ivc, layers=layers, pages=6 * n, kv_heads=kv, pt=pt, D_=D_, seqs=n, max_pages=6)
+    p.ws = ivc.new_workspace(ivc.cache_workspace_size(p.gpu, n, 70))
+    rng = np.random.RandomState(1)
+    lens = rng.randint(0, 20, n).tolist()
+    seqs = rng.permutation(n).tolist()
+    p.reserve(lens, seqs)
+    p.compact(lens, seqs=seqs)
+    p.reserve([70] * n, seqs)
+    keep = [sorted(rng.permutation(70)[:60].tolist()) for _ in range(n)]
+    count = [int(x) for x in rng.randint(0, 61, n)]
+    p.compact(count, keep, None, seqs)
