@@ -251,13 +251,12 @@ __global__ void __launch_bounds__(CA_THREADS)
   long long need = 0, total;
   for (int base = 0; base < n; base += CA_THREADS) need += read(base, true);
   block_scan(need, sh.warp_sum, total);
-  if (tid == 0 && total > fc) sh.bad |= DEV_CACHE_FULL;
-  bool go = still_good(sh) && total > 0;
-  if (go) {
+  if (total > fc) {
+    if (tid == 0) sh.bad |= DEV_CACHE_FULL;
+  } else if (fc <= c.pages) {
     check_top(c, sh, taken, fc, static_cast<int>(total));
-    go = still_good(sh);
   }
-  if (go) {
+  if (still_good(sh) && total > 0) {
     long long carry = 0;
     for (int base = 0; base < n; base += CA_THREADS) {
       if (n > CA_THREADS) read(base, false);
