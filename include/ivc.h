@@ -347,7 +347,8 @@ int ivc_assemble_sequence(const int32_t* input_ids, const int32_t* seq_offsets, 
  * A page may belong to several sequences (ref[p] counts them) once a fork
  * shared it: such pages are full, and no call writes into them.
  *   page_tokens 16, 32, 64 or 128; head_dim 64 or 128; pages <= 2^20;
- *   max_seqs <= 65536; one layer's pages * kv_heads * page_tokens < 2^31.
+ *   max_seqs <= 65536; layers <= 4096; kv_heads <= 1024; max_pages * page_tokens
+ *   <= 2^30; one layer's pages * kv_heads * page_tokens < 2^31.
  * All pointers are caller-owned device memory; k and v 16-byte aligned. Calls
  * that change a cache, and calls that read what another one changes, are
  * ordered by the caller (one stream, or events).
@@ -373,8 +374,10 @@ int ivc_cache_init(const ivc_cache* c, ivc_stream_t stream);
 
 /* Page operations. `seqs` (device int32 [n], NULL: sequences 0 .. n-1) names
  * sequences of the cache, each at most once. A call either does all of its
- * work or, when the device data are wrong (IVC_DEV_BAD_CACHE) or the pages do
- * not suffice (IVC_DEV_CACHE_FULL), none of it. The results do not depend on
+ * work or, when the device data that it touches are wrong (IVC_DEV_BAD_CACHE: its
+ * arguments, a page number, a page to take that is held or listed twice, a page to
+ * give back with fewer holders than give it back, no room on the free list) or the
+ * pages do not suffice (IVC_DEV_CACHE_FULL), none of it. The results do not depend on
  * the order in which threads run: pages are taken from the top of the free
  * list in the order of `seqs`, and given back so that the lowest number of
  * those freed by the call is taken next.
@@ -423,7 +426,8 @@ int ivc_cache_free(const ivc_cache* c, const int32_t* seqs, int n, void* workspa
  *   q_out      device bf16 [N, q_heads, head_dim].
  * A sequence may be named once (two rows would store to one place). A token
  * behind the pages that the sequence holds is not stored (IVC_DEV_BAD_CACHE);
- * bad offsets set IVC_DEV_BAD_TREE. q_heads a multiple of kv_heads. */
+ * bad offsets set IVC_DEV_BAD_TREE. q_heads a multiple of kv_heads, at most 65536;
+ * N <= 2^28. */
 int ivc_qk_norm_rope(const ivc_cache* c, int layer, const void* qkv, long long ld, int N,
                      int q_heads, const void* q_gamma, const void* k_gamma, float eps, double theta,
                      const int32_t* positions, const int32_t* offsets, const int32_t* seqs, int B,
@@ -467,8 +471,13 @@ int ivc_tree_attention(const ivc_cache* c, int layer, const void* q, long long q
  * After the last standing node the next token is drawn from r: the least v with
  * sum_{t <= v} r(t) > u_next[b] sum(r). Where sum(r) is 0 it is drawn from the
  * node's p. A later sibling is not tried once z <= 0. All of this in fp64 from
- * the fp32 inputs; entries of p and q that are not positive (NaN included)
- * count as 0.
+ * the fp32 inputs, products and differences rounded as written (1 / z and 1 / w
+ * once), sums in an order of the kernel's own that is the same from call to call;
+ * entries of p and q that are not positive (NaN included) count as 0. Rows are taken
+ * to sum to 1: what fp32 rows miss of that is missed by z and w too. Where q is
+ * given a rejection costs a pass over the vocabulary that repeats the node's
+ * rejections before it, so a node the square of their number.
+ * V <= 2^28; B <= 2^24.
  *   p, q    device fp32 [N, V], rows p_ld / q_ld elements apart.
  *   tokens, parents  device int32 [N]; parents as in ivc_tree_attention
  *           (NULL: chains), but node 0 is the only root: nodes that do not

@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(CA_THREADS)
 // with them, so a chunk of rows that is read whole before any of it is written
 // cannot spoil a later chunk's sources; the next chunk's loads are issued before
 // this one's stores (its sources lie behind these targets). Bound by HBM: 848 of 3390
-// tokens of three sequences in 36 layers, 0.7 GB read and written, take 145 us.
+// tokens of three sequences in 36 layers, 0.7 GB read and written, take 149 us.
 constexpr int MV_THREADS = 256;
 constexpr int MV_PIECES = 4;  // 16-byte pieces a thread holds of a chunk
 constexpr int MV_CTAS = 8;

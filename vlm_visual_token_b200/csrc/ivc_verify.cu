@@ -9,20 +9,26 @@
 // when its last rejection just made that pass).
 //
 // r is a function of the row's fp32 inputs and the scalars z_i, w_i, c_i of the
-// node's rejections so far, so every pass recomputes it in fp64 from the inputs:
-// nothing is stored and nothing rounded in between. Sums are fp64 in a fixed order.
+// node's rejections so far, so every pass recomputes it in fp64 from the inputs, with
+// the formula's roundings: nothing is stored. The n-th rejection at a node repeats the
+// n - 1 before it for every value, so a node costs the square of its rejections: a
+// star of 128 nodes over 151001 tokens that are all rejected takes 7.5 ms. Sums are
+// fp64 in a fixed order (per lane, warp, slice), which is not the order of the tokens:
+// results are the same from call to call, and the formula's up to the rounding of sums.
 //
 // A sequence is one cluster of 8 CTAs: each walks for itself (the same scalars) and
 // sums a contiguous eighth of the vocabulary, and the eight sums are exchanged
 // through distributed shared memory. One sequence without a rejection is bound by
-// its chain of dependent loads (offsets, tokens, probabilities, row): 7 us for 151001
-// tokens. A rejection with draft probabilities adds a pass of about 4 us, bound by
-// the fp64 and conversion pipes of the cluster's SMs;
-// a batch takes as long as its longest chain of them: 48 trees of 16 nodes 55 us,
-// without rejections 16 us (their rows in one read from HBM would be 9 us).
-// 384 threads of 80 registers: 512 threads spill, 256 take 8.1 us for one sequence.
-// Clusters of 16 halve a pass but fewer fit: 52 us for the trees, 19 us without
-// rejections.
+// its chain of dependent loads (offsets, tokens, probabilities, row): 6.8 us for 151001
+// tokens. A rejection with draft probabilities adds a pass, bound by the fp64 and
+// conversion pipes of the cluster's SMs: 7 rejections of one node 57 us, 15 of them
+// 169 us. A batch takes as long as its longest chain of them, and 48 sequences'
+// clusters do not fit at once: 48 trees of 16 nodes 49 to 62 us by their inputs,
+// without drafts 17 us (their rows in one read from HBM would be 4), with 15 rejections
+// of the root each 435 us. (Device times over changing inputs.)
+// 384 threads of 80 registers: 512 threads spill, 256 were a sixth slower for one
+// sequence. Clusters of 16 halve a pass but fewer fit: for the trees a twentieth
+// faster, without rejections a fifth slower.
 #include <cuda_runtime.h>
 
 #include "ivc_internal.h"
@@ -34,7 +40,10 @@ namespace {
 constexpr int VF_THREADS = 384;
 constexpr int VF_WARPS = VF_THREADS / 32;
 constexpr int VF_CLUSTER = 8;
-constexpr int VF_SMALL = 4096;  // a vocabulary up to this size is one CTA's
+// A vocabulary up to this size is one CTA's: for 4096 tokens one sequence takes 4.1 us
+// (a cluster 4.8), with 7 rejections 21.6 (20.2), 48 of those 21.8 (37.9); for 8192 tokens
+// 4.6 (4.8), 26.7 (20.7) and 27.1 (38.8).
+constexpr int VF_SMALL = 4096;
 constexpr int VF_BATCH = 8;     // values a thread has in flight
 
 struct VerifyArgs {
@@ -398,7 +407,6 @@ extern "C" int ivc_verify_drafts(const float* p, long long p_ld, const float* q,
                      path, path_stride, n_path, next_token, static_cast<int*>(workspace)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   TraceScope ts("verify_drafts", s);
-  // small vocabularies: one CTA (no cluster to wait for)
   if (V <= VF_SMALL) return launch_k(verify_kernel<1>, dim3(B), dim3(VF_THREADS), 0, s, 1, a);
   return launch_k(verify_kernel<VF_CLUSTER>, dim3(static_cast<unsigned>(B) * VF_CLUSTER),
                   dim3(VF_THREADS), 0, s, VF_CLUSTER, a);
