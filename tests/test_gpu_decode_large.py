@@ -242,3 +242,34 @@ def test_compaction_with_several_heads_per_cta(kv, layers, n, D_):
     keep = [sorted(rng.permutation(70)[:60].tolist()) for _ in range(n)]
     count = [int(x) for x in rng.randint(0, 61, n)]
     p.compact(count, keep, None, seqs)
+
+
+def test_the_largest_cache():
+    """2^20 pages, the most that a cache may have: all of them taken, shared, given back."""
+    ivc = _ivc()
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("needs 4 GB of device memory")
+    pages, row = 1 << 20, 1 << 16            # a sequence's 65536 pages of 16 tokens
+    c = ivc.Cache.empty(1, pages, 1, 16, 64, 20, row)
+    ws = ivc.new_workspace(ivc.cache_workspace_size(c, 16, 0))
+    full = dev([16 * row] * 16)
+    ivc.cache_reserve(c, full, workspace=ws)
+    ivc.cache_compact(c, full, workspace=ws)
+    assert ivc.device_status(ws) == 0 and int(c.free_count) == 0
+    held = torch.arange(pages, dtype=torch.int32, device="cuda")
+    assert torch.equal(c.table[:16].reshape(-1), held) and (c.ref == 1).all()
+    ivc.cache_reserve(c, dev([1]), dev([16]), workspace=ws)
+    assert ivc.device_status(ws) == 64
+    ivc.cache_fork(c, dev([3, 3]), dev([16, 17]), workspace=ws)     # every page is full: none is needed
+    ivc.cache_fork(c, dev([3]), dev([18]), False, workspace=ws)     # and none is there to copy to
+    assert ivc.device_status(ws) == 64
+    assert torch.equal(c.table[16], c.table[3]) and (c.ref[3 * row:4 * row] == 3).all()
+    ivc.cache_free(c, dev([3, 0, 15, 16]), workspace=ws)
+    assert ivc.device_status(ws) == 0 and int(c.free_count) == 2 * row
+    assert torch.equal(c.free_list[:2 * row], torch.cat([held[15 * row:].flip(0), held[:row].flip(0)]))
+    ivc.cache_fork(c, dev([17, 7]), dev([18, 19]), False, workspace=ws)
+    assert ivc.device_status(ws) == 0 and int(c.free_count) == 0
+    assert torch.equal(c.table[18], held[:row]) and torch.equal(c.table[19], held[15 * row:])
+    ivc.cache_free(c, dev([17, 18, 19, 1, 2, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14]), workspace=ws)
+    assert ivc.device_status(ws) == 0 and int(c.free_count) == pages and (c.ref == 0).all()
+    assert torch.equal(c.free_list.sort().values, held) and (c.table == -1).all()
