@@ -14,3 +14,33 @@ def test_a_scale_that_overflows_in_log2_units_is_refused(scale):
                                           need - 1, None)
     assert call(scale) == EINVAL
     assert call(2e38) == -3                  # allowed: the next check, the workspace's size, refuses
+
+
+def test_device_status_reads_on_the_workspaces_device(monkeypatch):
+    """With another device current: its stream is not behind the calls that set the bits."""
+    import contextlib
+    import types
+
+    import torch
+
+    import vlm_visual_token_b200 as ivc
+    current, used = [0], []
+
+    @contextlib.contextmanager
+    def device(d):
+        before, current[0] = current[0], torch.device(d).index
+        yield
+        current[0] = before
+
+    def status(ws, bits, stream):
+        used.append((ws.value if hasattr(ws, "value") else ws, stream.value))
+        bits._obj.value = 64
+        return -5
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_stream",
+                        lambda d=None: types.SimpleNamespace(cuda_stream=100 + current[0]))
+    monkeypatch.setattr(ivc, "lib", lambda: types.SimpleNamespace(ivc_device_status=status))
+    ws = types.SimpleNamespace(device=torch.device("cuda:1"), data_ptr=lambda: WS)
+    assert ivc.device_status(ws) == 64
+    assert used == [(WS, 101)] and current == [0]

@@ -374,9 +374,11 @@ def assemble_sequence(input_ids: torch.Tensor, seq_offsets: torch.Tensor, img_co
 
 
 def device_status(workspace: torch.Tensor, stream=None) -> int:
-    """Bits of the workspace's device status word (then cleared)."""
+    """Bits of the workspace's device status word (then cleared), once `stream`
+    (default: the current stream of the workspace's device) has come to here."""
     bits = ctypes.c_int(0)
-    rc = lib().ivc_device_status(_ptr(workspace), ctypes.byref(bits), _stream(stream))
+    with torch.cuda.device(workspace.device):
+        rc = lib().ivc_device_status(_ptr(workspace), ctypes.byref(bits), _stream(stream))
     if rc not in (0, -5):
         raise IvcError(rc, "ivc_device_status")
     return bits.value
